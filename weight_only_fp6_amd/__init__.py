@@ -17,6 +17,11 @@ call takes ``fmt`` ("e3m2" -- the default, FP6 -- "e2m3", "e2m2" or "e2m1"):
 * 2:4-sparse FP6 (``include/fp6s.h``): :func:`sparse_packed_bytes`,
   :func:`prune_quantize`, :func:`sparse_prepack`, :func:`sparse_linear`,
   :func:`sparse_linear_plan`, :func:`sparse_dequant`
+* 8-bit integer linear layer (``include/fp6_int8.h``): :func:`int8_padded_k`,
+  :func:`int8_quantize_rows` (host), :func:`int8_quantize_tokens`,
+  :func:`int8_linear`
+* mixture-of-experts layer for few tokens (``include/fpx_moe.h``):
+  :func:`moe_prepack` (host), :func:`moe_layer`, :func:`moe_experts`
 
 There is no fallback: if the shared library is missing or fails to load,
 importing this package raises.
@@ -43,6 +48,9 @@ EXPORTED = (
     "fp6_release", "fpx_bits", "fpx_packed_bytes", "fpx_quantize_rows", "fpx_prepack",
     "fpx_linear", "fpx_linear_plan", "fpx_dequant", "fp6s_packed_bytes", "fp6s_prune_quantize",
     "fp6s_prepack", "fp6s_linear", "fp6s_linear_plan", "fp6s_linear_plan_query", "fp6s_dequant",
+    "fp6_int8_padded_k", "fp6_int8_quantize_rows", "fp6_int8_quantize_tokens", "fp6_int8_linear",
+    "fp6_int8_workspace_bytes", "fp6_int8_linear_tokens", "fpx_moe_workspace_bytes", "fpx_moe_experts",
+    "fpx_moe_layer",
 )
 FORMATS = {"e3m2": 0, "e2m3": 1, "e2m2": 2, "e2m1": 3}
 
@@ -94,6 +102,15 @@ def _load() -> ctypes.CDLL:
         "fp6s_linear_plan": ([vp, vp, vp, vp, i64, i64, i64, i32, i32, vp], i32),
         "fp6s_linear_plan_query": ([i64, i64, i64, ctypes.POINTER(i32), ctypes.POINTER(i32)], i32),
         "fp6s_dequant": ([vp, vp, vp, i64, i64, vp], i32),
+        "fp6_int8_padded_k": ([i64], i64),
+        "fp6_int8_quantize_rows": ([vp, i64, i64, vp, vp], i32),
+        "fp6_int8_quantize_tokens": ([i32, vp, i64, i64, i64, vp, vp, vp], i32),
+        "fp6_int8_linear": ([vp, vp, vp, vp, vp, i32, vp, i64, i64, i64, vp], i32),
+        "fp6_int8_workspace_bytes": ([i64, i64], sz),
+        "fp6_int8_linear_tokens": ([i32, vp, i64, vp, vp, vp, i32, vp, i64, i64, i64, vp, sz, vp], i32),
+        "fpx_moe_workspace_bytes": ([i64, i64, i64, i64, i64], sz),
+        "fpx_moe_experts": ([i32, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, sz, vp], i32),
+        "fpx_moe_layer": ([i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, i64, i64, i64, i64, i64, vp, sz, vp], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -352,6 +369,252 @@ def sparse_dequant(packed, scales, N: int, K: int, out=None, stream=None):
     st = _lib.fp6s_dequant(_dev_ptr(packed), _dev_ptr(scales), _dev_ptr(out), N, K, _stream_handle(stream))
     _check("fp6s_dequant", st)
     return out
+
+
+# ---------------------------------------------------------------------------
+# 8-bit integer linear layer and mixture-of-experts layer.  These calls launch
+# kernels of a few microseconds, so their checks are written out instead of
+# going through _check_device_tensors, and they run on the device and (by
+# default) the current stream of their first tensor.
+# ---------------------------------------------------------------------------
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _gpu_tensor(t, dtype, shape, device, what: str) -> int:
+    """The address of a contiguous tensor of that dtype and shape on `device`
+    (None: any GPU), else ValueError."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{what} must be on the GPU" + (f" {device}, as the first argument" if device else ""))
+    return t.data_ptr()
+
+
+class _Launch:
+    """Device and stream of one call: makes `device` current and, where the
+    caller gave a stream, makes that current too, so that outputs and workspaces
+    belong to the stream that uses them."""
+
+    def __init__(self, device, stream):
+        import torch
+        self._scopes = []
+        if device.index != torch.cuda.current_device():
+            self._scopes.append(torch.cuda.device(device))
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            self._scopes.append(torch.cuda.stream(stream))
+        self._device = device
+
+    def __enter__(self):
+        import torch
+        for s in self._scopes:
+            s.__enter__()
+        return torch.cuda.current_stream(self._device).cuda_stream
+
+    def __exit__(self, *exc):
+        for s in reversed(self._scopes):
+            s.__exit__(*exc)
+
+
+def int8_padded_k(K: int) -> int:
+    """Bytes of a code row: K rounded up to a multiple of 16 (0: K is out of range)."""
+    return int(_lib.fp6_int8_padded_k(K))
+
+
+def int8_quantize_rows(W: np.ndarray):
+    """Host quantiser: float32 [N,K] -> (codes int8 [N,Kp], zero from K on; scales float32 [N])."""
+    W = np.ascontiguousarray(W, dtype=np.float32)
+    if W.ndim != 2:
+        raise ValueError("W must be 2-D")
+    N, K = W.shape
+    codes = np.empty((N, int8_padded_k(K)), dtype=np.int8)
+    scales = np.empty(N, dtype=np.float32)
+    _check("fp6_int8_quantize_rows",
+           _lib.fp6_int8_quantize_rows(_host_ptr(W), N, K, _host_ptr(codes), _host_ptr(scales)))
+    return codes, scales
+
+
+def _token_rows(X):
+    """dtype id, row stride and address of fp16/bf16 rows [M,K] whose elements lie side by side."""
+    import torch
+    if not isinstance(X, torch.Tensor) or X.dim() != 2 or X.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("X must be an fp16 or bf16 [M,K] tensor")
+    M, K = X.shape
+    sm, sk = X.stride()
+    _need(K >= 1 and (sk == 1 or K == 1), "the elements of a row of X must lie side by side")
+    if M <= 1:
+        sm = K
+    _need(sm >= K, "rows of X must not overlap")
+    _need(X.is_cuda, "X must be on the GPU")
+    return (0 if X.dtype == torch.float16 else 1), sm, X.data_ptr()
+
+
+def int8_quantize_tokens(X, out=None, scales=None, stream=None):
+    """fp16/bf16 [M,K] -> (codes int8 [M,Kp], zero from K on; scales float32 [M]), one scale
+    per row: q = RNE(127 x / max|x|).  Rows of X may be a part of wider ones."""
+    import torch
+    dt, ldx, px = _token_rows(X)
+    M, K = X.shape
+    kp = int8_padded_k(K)
+    _need(kp > 0, f"K = {K} is out of range")
+    with _Launch(X.device, stream) as s:
+        if out is None:
+            out = torch.empty((M, kp), dtype=torch.int8, device=X.device)
+        if scales is None:
+            scales = torch.empty((M,), dtype=torch.float32, device=X.device)
+        pq = _gpu_tensor(out, torch.int8, (M, kp), X.device, "out")
+        ps = _gpu_tensor(scales, torch.float32, (M,), X.device, "scales")
+        _check("fp6_int8_quantize_tokens", _lib.fp6_int8_quantize_tokens(dt, px, ldx, M, K, pq, ps, s))
+    return out, scales
+
+
+def int8_linear(X, W, w_scales, x_scales=None, bias=None, out=None, out_dtype=None, stream=None):
+    """Y[M,N] = (X . W^T) * w_scales * x_scales (+ bias) with int8 operands.
+
+    X: int8 codes [M,Kp] with ``x_scales`` float32 [M] (of :func:`int8_quantize_tokens`), or
+    fp16/bf16 activations [M,K], which the call quantises first.  W: int8 codes [N,Kp], w_scales
+    float32 [N].  Y and bias [N] are fp16 or bf16: ``out``'s dtype, else ``out_dtype``, else X's
+    (codes: fp16).
+    """
+    import torch
+    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("W must be an int8 [N,Kp] tensor")
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X must be an int8 [M,Kp] or an fp16 or bf16 [M,K] tensor")
+    N, kp = W.shape
+    M, K = X.shape
+    codes = X.dtype == torch.int8
+    dev = X.device
+    if codes:
+        _need(x_scales is not None, "codes need x_scales")
+        px = _gpu_tensor(X, torch.int8, (M, kp), None, "X")
+        psx = _gpu_tensor(x_scales, torch.float32, (M,), dev, "x_scales")
+        _need(kp % 16 == 0 and 16 <= kp == int8_padded_k(kp), f"Kp = {kp} is not the size of a padded code row")
+    else:
+        _need(x_scales is None, "x_scales belong to int8 codes")
+        dt, ldx, px = _token_rows(X)
+        _need(0 < kp == int8_padded_k(K), f"W must have {int8_padded_k(K)} codes in a row for K = {K}, got {kp}")
+    if out is not None:
+        _need(isinstance(out, torch.Tensor), "out must be a tensor")
+        _need(out_dtype is None or out_dtype == out.dtype, "out has another dtype than out_dtype")
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = torch.float16 if codes else X.dtype
+    _need(out_dtype in (torch.float16, torch.bfloat16), "the output is fp16 or bf16")
+    od = 0 if out_dtype == torch.float16 else 1
+    pw = _gpu_tensor(W, torch.int8, (N, kp), dev, "W")
+    psw = _gpu_tensor(w_scales, torch.float32, (N,), dev, "w_scales")
+    pb = 0 if bias is None else _gpu_tensor(bias, out_dtype, (N,), dev, "bias")
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        py = _gpu_tensor(out, out_dtype, (M, N), dev, "out")
+        if codes:
+            st = _lib.fp6_int8_linear(px, psx, pw, psw, pb, od, py, M, N, kp, s)
+        else:
+            nbytes = M * kp + 4 * M
+            ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+            st = _lib.fp6_int8_linear_tokens(dt, px, ldx, pw, psw, pb, od, py, M, N, K, ws.data_ptr(), nbytes, s)
+        _check("fp6_int8_linear" if codes else "fp6_int8_linear_tokens", st)
+    return out
+
+
+def moe_prepack(codes: np.ndarray, scales: np.ndarray, fmt: str = "e3m2") -> np.ndarray:
+    """Host packer of a stack of experts: codes uint8 [E,N,K] + scales fp16 [E,N] -> uint8
+    [E, N*K*bits/8], each expert as :func:`prepack` packs it (experts are packed in parallel)."""
+    from concurrent.futures import ThreadPoolExecutor
+    codes = np.ascontiguousarray(codes, dtype=np.uint8)
+    scales = np.ascontiguousarray(scales, dtype=np.float16)
+    if codes.ndim != 3 or scales.shape != codes.shape[:2]:
+        raise ValueError("codes [E,N,K] and scales [E,N] expected")
+    E, N, K = codes.shape
+    f, nbytes = _fmt_id(fmt), packed_bytes(N, K, fmt)
+    out = np.empty((E, nbytes), dtype=np.uint8)
+
+    def pack(e):
+        return _lib.fpx_prepack(f, _host_ptr(codes[e]), _host_ptr(scales[e]), N, K, _host_ptr(out[e]), nbytes)
+
+    with ThreadPoolExecutor(max_workers=min(16, max(E, 1))) as pool:
+        for st in pool.map(pack, range(E)):
+            _check("moe_prepack", st)
+    return out
+
+
+def _moe_args(X, gate_up, gate_up_scales, down, down_scales, fmt):
+    """Sizes and addresses of the experts of a call: (format, T, E, H, I, x, gate_up, scales, down, scales)."""
+    import torch
+    f = _fmt_id(fmt)
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X must be an fp16 [T,H] tensor")
+    for t, what in ((gate_up_scales, "gate_up_scales"), (down_scales, "down_scales")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError(f"{what} must be an fp16 tensor with a row for each expert")
+    T, H = X.shape
+    E, I = gate_up_scales.shape[0], gate_up_scales.shape[1] // 2
+    f16, dev = torch.float16, X.device
+    nbytes = packed_bytes(H, I, fmt)
+    return (f, T, E, H, I, _gpu_tensor(X, f16, (T, H), None, "X"),
+            _gpu_tensor(gate_up, torch.uint8, (E, packed_bytes(2 * I, H, fmt)), dev, "gate_up (the moe_prepack output)"),
+            _gpu_tensor(gate_up_scales, f16, (E, 2 * I), dev, "gate_up_scales"),
+            _gpu_tensor(down, torch.uint8, (E, nbytes), dev, "down (the moe_prepack output)"),
+            _gpu_tensor(down_scales, f16, (E, H), dev, "down_scales"))
+
+
+def moe_experts(X, ids, weights, gate_up, gate_up_scales, down, down_scales, fmt: str = "e3m2", out=None,
+                stream=None):
+    """Y[t] = sum_j down[ids[t,j]] . (weights[t,j] * silu(gate X[t]) * up X[t]), fp16 [T,H].
+
+    ids int32 [T,top_k] (outside [0,E): that choice is not served here), weights float32 [T,top_k];
+    gate_up and down: :func:`moe_prepack` of [E,2I,H] (gate rows, then up rows) and [E,H,I].
+    """
+    import torch
+    f, T, E, H, I, px, pg, pgs, pd, pds = _moe_args(X, gate_up, gate_up_scales, down, down_scales, fmt)
+    dev = X.device
+    _need(isinstance(ids, torch.Tensor) and ids.dim() == 2, "ids must be an int32 [T,top_k] tensor")
+    k = ids.shape[1]
+    pi = _gpu_tensor(ids, torch.int32, (T, k), dev, "ids")
+    pw = _gpu_tensor(weights, torch.float32, (T, k), dev, "weights")
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.float16, device=dev)
+        py = _gpu_tensor(out, torch.float16, (T, H), dev, "out")
+        nbytes = _lib.fpx_moe_workspace_bytes(T, E, k, H, I)
+        ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        _check("fpx_moe_experts", _lib.fpx_moe_experts(f, px, pi, pw, pg, pgs, pd, pds, py, T, E, k, H, I,
+                                                       ws.data_ptr(), nbytes, s))
+    return out
+
+
+def moe_layer(X, router, gate_up, gate_up_scales, down, down_scales, top_k: int, renormalize: bool = True,
+              fmt: str = "e3m2", out=None, stream=None):
+    """The whole layer for few tokens -> (Y fp16 [T,H], ids int32 [T,top_k], weights float32 [T,top_k]).
+
+    The router (fp16 [E,H]) chooses each token's top_k experts by 64-bit logits, ties to the lower
+    index; weights are the softmax over all experts, divided by the chosen ones' sum where
+    ``renormalize``.  The experts are those of :func:`moe_experts`.
+    """
+    import torch
+    f, T, E, H, I, px, pg, pgs, pd, pds = _moe_args(X, gate_up, gate_up_scales, down, down_scales, fmt)
+    dev = X.device
+    pr = _gpu_tensor(router, torch.float16, (E, H), dev, "router")
+    k = int(top_k)
+    _need(1 <= k <= E, f"top_k = {k} is not in 1 .. {E}")
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.float16, device=dev)
+        py = _gpu_tensor(out, torch.float16, (T, H), dev, "out")
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        nbytes = _lib.fpx_moe_workspace_bytes(T, E, k, H, I)
+        ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        _check("fpx_moe_layer", _lib.fpx_moe_layer(f, px, pr, pg, pgs, pd, pds, 1 if renormalize else 0, py,
+                                                   ids.data_ptr(), weights.data_ptr(), T, E, k, H, I,
+                                                   ws.data_ptr(), nbytes, s))
+    return out, ids, weights
 
 
 def release() -> None:

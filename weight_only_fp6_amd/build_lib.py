@@ -1,9 +1,9 @@
 """Build the HIP library ``libfp6amd.so`` in-tree for gfx950.
 
-Host code (fp6_host.cpp) is compiled with g++; the host dispatch and device
-entry points (fpx_linear.hip) and the kernels, one translation unit per
-weight format (fpx_kern_*.hip, compiled in parallel), with hipcc; all are
-linked into one shared library next to this file.  Run
+Host code (fp6_host.cpp, int8_host.cpp) is compiled with g++; the host
+dispatch and device entry points (fpx_linear.hip), the kernels, one
+translation unit per weight format (fpx_kern_*.hip, compiled in parallel), and
+the sparse, int8 and mixture-of-experts layers with hipcc; all are linked into one shared library next to this file.  Run
 ``python weight_only_fp6_amd/build_lib.py`` (by path, so the package -- which
 loads the library -- is not imported first).
 """
@@ -48,7 +48,8 @@ def _run(cmd, verbose):
 
 
 HIP_SOURCES = ["fpx_linear.hip", "fpx_kern_e3m2.hip", "fpx_kern_e2m3.hip", "fpx_kern_e2m2.hip",
-               "fpx_kern_e2m1.hip", "fpx_sparse.hip"]
+               "fpx_kern_e2m1.hip", "fpx_sparse.hip", "int8_linear.hip", "fpx_moe.hip"]
+HOST_SOURCES = ["fp6_host.cpp", "int8_host.cpp"]
 
 
 def _run_parallel(cmds, verbose):
@@ -71,9 +72,11 @@ def build(verbose: bool = False) -> str:
     """Compile and link the library; returns its path.  Always rebuilds."""
     os.makedirs(BUILD, exist_ok=True)
     inc = ["-I", INCLUDE, "-I", CSRC]
-    host_o = os.path.join(BUILD, "fp6_host.o")
-    objs = [host_o]
-    cmds = [["g++", *HOST_FLAGS, *inc, "-c", os.path.join(CSRC, "fp6_host.cpp"), "-o", host_o]]
+    objs, cmds = [], []
+    for src in HOST_SOURCES:
+        obj = os.path.join(BUILD, src.replace(".cpp", ".o"))
+        objs.append(obj)
+        cmds.append(["g++", *HOST_FLAGS, *inc, "-c", os.path.join(CSRC, src), "-o", obj])
     for src in HIP_SOURCES:
         obj = os.path.join(BUILD, src.replace(".hip", ".o"))
         objs.append(obj)
