@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "fp6_int8.h"
 #include "fp6_limits.h"
@@ -148,29 +149,41 @@ __global__ __launch_bounds__(256) void i8_quantize(const uint16_t* __restrict__ 
 // ---------------------------------------------------------------------------
 // Epilogue: y = (acc * sw) * sx (+ bias) in fp32, one rounding.
 // ---------------------------------------------------------------------------
-template <int DT>
-__device__ __forceinline__ void store4(void* Y, const i32x4& acc, float sx, const float* __restrict__ sw,
-                                       const void* __restrict__ bias, int64_t m, int64_t n, int64_t M,
-                                       int64_t N) {
+// acc[i][j], lane (r, g): channels n + 16 i + 0..3 of token m + 16 j, with
+// n already at the lane's channels and m at its token.  WHOLE: no edge, N % 4 == 0.
+template <int DT, int TA, int TB, bool WHOLE>
+__device__ __forceinline__ void store_tile(void* __restrict__ Y, const i32x4 (&acc)[TA][TB], const float* __restrict__ sx,
+                                           const float* __restrict__ sw, const void* __restrict__ bias, int64_t m,
+                                           int64_t n, int64_t M, int64_t N) {
   using T = typename Elem<DT>::T;
   typedef T T4 __attribute__((ext_vector_type(4)));
-  if (m >= M) return;
-  T* y = static_cast<T*>(Y) + m * N + n;
   const T* b = static_cast<const T*>(bias);
-  T4 o;
+  float xs[TB];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t ni = n + i < N ? n + i : N - 1;
-    float v = (static_cast<float>(acc[i]) * sw[ni]) * sx;
-    if (b) v += static_cast<float>(b[ni]);
-    o[i] = static_cast<T>(v);
-  }
-  if ((N & 3) == 0 && n + 4 <= N) {
-    *reinterpret_cast<T4*>(y) = o;
-  } else {
+  for (int j = 0; j < TB; ++j) xs[j] = sx[WHOLE || m + 16 * j < M ? m + 16 * j : M - 1];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < N) y[i] = o[i];
+  for (int i = 0; i < TA; ++i) {
+    float ws[4], bs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t ni = n + 16 * i + e;
+      ws[e] = sw[WHOLE || ni < N ? ni : N - 1];
+      if (b) bs[e] = static_cast<float>(b[WHOLE || ni < N ? ni : N - 1]);
+    }
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      T4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = static_cast<T>((static_cast<float>(acc[i][j][e]) * ws[e]) * xs[j] + bs[e]);
+      T* y = static_cast<T*>(Y) + (m + 16 * j) * N + n + 16 * i;
+      if constexpr (WHOLE) {
+        *reinterpret_cast<T4*>(y) = o;
+      } else if (m + 16 * j < M) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + 16 * i + e < N) y[e] = o[e];
+      }
+    }
   }
 }
 
@@ -264,9 +277,162 @@ __global__ __launch_bounds__(512) void i8_skinny(const int8_t* __restrict__ Xq, 
 #pragma unroll
     for (int v = 1; v < kWaves; ++v) sum += red[v][i][lane];
     const int a = i / MB, b = i % MB;
-    const int64_t m = m0 + 16 * b + r;
-    const float s = sx[m < M ? m : M - 1];
-    store4<DT>(Y, sum, s, sw, bias, m, n0 + 16 * a + 4 * g, M, N);
+    const int64_t m = m0 + 16 * b + r, n = n0 + 16 * a + 4 * g;
+    const i32x4 one[1][1] = {{sum}};
+    if ((N & 3) == 0 && m < M && n < N) {
+      store_tile<DT, 1, 1, true>(Y, one, sx, sw, bias, m, n, M, N);
+    } else {
+      store_tile<DT, 1, 1, false>(Y, one, sx, sw, bias, m, n, M, N);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tiled product (many tokens).  A workgroup of WA x WB waves owns a tile of
+// 16*WA*TA channels x 16*WB*TB tokens, a wave 16*TA x 16*TB of it.  K runs in
+// steps of 64 bytes through a ring of four LDS stages, filled by direct LDS
+// loads.  Step t multiplies fragments that are in registers, reads those of
+// step t+1 from LDS between the MFMAs, and requests step t+3 into the stage
+// that step t-1 left; one barrier per step, and a load has two steps to arrive.
+// Each stage is its own LDS array and the barrier carries no fence, so that
+// nothing waits for more loads than the next step needs.
+//
+// An LDS row is 64 bytes in four 16-byte units; unit c of row r lies at place
+// (c + r/2) % 4, so that 8 rows' fragment reads of one c cover 8 different
+// places of a 128-byte line.  The direct loads are linear on the LDS side, so
+// the turn is made on the global side.  Units behind a row's end (Kp need not
+// be a multiple of 64) are loaded from 16 bytes of zeros; rows behind the last
+// repeat it and are not stored.
+// ---------------------------------------------------------------------------
+__device__ const u32x4 kZeroUnit[1] = {};
+
+__device__ __forceinline__ void barrier_no_fence() { asm volatile("s_barrier" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // until at most N of the wave's loads are in flight
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// Workgroup index -> tile, XCD-aware: workgroups go to the 8 XCDs in turn, and
+// each XCD gets a contiguous range of the order below, in which kBand token
+// tiles by all channel tiles follow one another (they share channels' bytes in
+// the XCD's L2).
+__device__ __forceinline__ void tile_of(uint32_t b, uint32_t mt, uint32_t nt, uint32_t& tm, uint32_t& tn) {
+  constexpr uint32_t kXcds = 8, kBand = 8;
+  const uint32_t G = mt * nt, x = b % kXcds, j = b / kXcds, q = G / kXcds, r = G % kXcds;
+  const uint32_t l = x * q + (x < r ? x : r) + j;
+  const uint32_t band = l / (kBand * nt), in = l - band * kBand * nt;
+  const uint32_t rows = mt - band * kBand < kBand ? mt - band * kBand : kBand;
+  tn = in / rows;
+  tm = band * kBand + (in - tn * rows);
+}
+
+template <int DT, int WA, int WB, int TA, int TB>
+__global__ __launch_bounds__(64 * WA * WB) void i8_tiled(const int8_t* __restrict__ Xq, const float* __restrict__ sx,
+                                                         const int8_t* __restrict__ Wq, const float* __restrict__ sw,
+                                                         const void* __restrict__ bias, void* __restrict__ Y,
+                                                         int64_t M, int64_t N, int64_t kp) {
+  constexpr int kThreads = 64 * WA * WB, kRowsA = 16 * WA * TA, kRowsB = 16 * WB * TB;
+  constexpr int kUnits = (kRowsA + kRowsB) * 4, kLoads = kUnits / kThreads;
+  static_assert(kUnits % kThreads == 0, "every thread makes the same number of loads");
+  __shared__ i32x4 st0[kUnits], st1[kUnits], st2[kUnits], st3[kUnits];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = lane & 15, g = lane >> 4;
+  const int wa = wave / WB, wb = wave - wa * WB;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, static_cast<uint32_t>((M + kRowsB - 1) / kRowsB), static_cast<uint32_t>((N + kRowsA - 1) / kRowsA),
+          tm, tn);
+  const int64_t n0 = static_cast<int64_t>(tn) * kRowsA, m0 = static_cast<int64_t>(tm) * kRowsB;
+
+  // This thread's units of a stage: place p of row p/4 holds unit (p - row/2) % 4.
+  const int8_t* src[kLoads];
+  int unit[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int p = i * kThreads + tid, row = p >> 2;
+    unit[i] = ((p & 3) - (row >> 1)) & 3;
+    if (row < kRowsA) {
+      const int64_t n = n0 + row < N ? n0 + row : N - 1;
+      src[i] = Wq + n * kp + 16 * unit[i];
+    } else {
+      const int64_t m = m0 + row - kRowsA < M ? m0 + row - kRowsA : M - 1;
+      src[i] = Xq + m * kp + 16 * unit[i];
+    }
+  }
+  const int steps = static_cast<int>((kp + 63) >> 6);
+  const int tail_units = static_cast<int>(kp - (static_cast<int64_t>(steps - 1) << 6)) >> 4;  // 1..4
+  auto request = [&](i32x4* stage, int t) {
+    const int tt = t < steps ? t : steps - 1;  // behind the end: the last step again, never read
+    const bool tail = tt == steps - 1;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int8_t* from = src[i] + static_cast<int64_t>(tt) * 64;
+      if (tail && unit[i] >= tail_units) from = reinterpret_cast<const int8_t*>(&kZeroUnit[0]);
+      __builtin_amdgcn_global_load_lds(
+          static_cast<const void*>(from),
+          reinterpret_cast<__attribute__((address_space(3))) void*>(
+              reinterpret_cast<uintptr_t>(stage + i * kThreads + wave * 64)),
+          16, 0, 0);
+    }
+  };
+  const int place = (g + (r >> 1)) & 3;  // 16-row blocks start at multiples of 4 half-rows
+  const int at_a = (wa * TA * 16 + r) * 4 + place, at_b = (kRowsA + wb * TB * 16 + r) * 4 + place;
+  i32x4 fa[2][TA], fb[2][TB], acc[TA][TB] = {};
+  auto read = [&](const i32x4* stage, i32x4 (&a)[TA], i32x4 (&b)[TB]) {
+#pragma unroll
+    for (int j = 0; j < TB; ++j) b[j] = stage[at_b + 64 * j];
+#pragma unroll
+    for (int i = 0; i < TA; ++i) a[i] = stage[at_a + 64 * i];
+  };
+  auto step = [&](int t, i32x4* next, i32x4* free_stage, auto P) {
+    constexpr int p = decltype(P)::value;
+    wait_loads<kLoads>();
+    barrier_no_fence();
+    request(free_stage, t + 3);
+    __builtin_amdgcn_sched_barrier(0);
+    read(next, fa[1 - p], fb[1 - p]);
+#pragma unroll
+    for (int i = 0; i < TA; ++i)
+#pragma unroll
+      for (int j = 0; j < TB; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[p][i], fb[p][j], acc[i][j], 0, 0, 0);
+    // MFMAs, then the one fragment read that falls to them: the wait before
+    // the first MFMA finds only the previous step's reads, long done.
+    constexpr int kReads = TA + TB, kPer = TA * TB / kReads > 0 ? TA * TB / kReads : 1;
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, TA * TB, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  request(st0, 0);
+  request(st1, 1);
+  request(st2, 2);
+  wait_loads<2 * kLoads>();
+  barrier_no_fence();
+  read(st0, fa[0], fb[0]);
+  constexpr std::integral_constant<int, 0> even{};
+  constexpr std::integral_constant<int, 1> odd{};
+  int t = 0;
+  for (; t + 4 <= steps; t += 4) {
+    step(t, st1, st3, even);
+    step(t + 1, st2, st0, odd);
+    step(t + 2, st3, st1, even);
+    step(t + 3, st0, st2, odd);
+  }
+  if (t < steps) step(t, st1, st3, even);
+  if (t + 1 < steps) step(t + 1, st2, st0, odd);
+  if (t + 2 < steps) step(t + 2, st3, st1, even);
+  __builtin_amdgcn_s_waitcnt(0);  // no load may land after the workgroup has left
+
+  const bool whole = (N & 3) == 0 && n0 + kRowsA <= N && m0 + kRowsB <= M;
+  const int64_t nw = n0 + wa * TA * 16 + 4 * g, mw = m0 + wb * TB * 16 + r;
+  if (whole) {
+    store_tile<DT, TA, TB, true>(Y, acc, sx, sw, bias, mw, nw, M, N);
+  } else {
+    store_tile<DT, TA, TB, false>(Y, acc, sx, sw, bias, mw, nw, M, N);
   }
 }
 
@@ -330,8 +496,25 @@ int launch_skinny(const Product& p, hipStream_t s) {
   return FP6_OK;
 }
 
+template <int DT, int WA, int WB, int TA, int TB>
+int launch_tiled(const Product& p, hipStream_t s) {
+  const int8_t *x = static_cast<const int8_t*>(p.xq), *w = static_cast<const int8_t*>(p.wq);
+  const float *sx = static_cast<const float*>(p.sx), *sw = static_cast<const float*>(p.sw);
+  const void* bias = p.bias;
+  void* y = p.y;
+  int64_t M = p.M, N = p.N, kp = p.kp;
+  void* args[] = {&x, &sx, &w, &sw, &bias, &y, &M, &N, &kp};
+  // At most 2^36 / 2^12 tiles of 64 * 64 or more, under 2^32 threads in all... 
+  const int64_t tiles = ceil_div(M, 16 * WB * TB) * ceil_div(N, 16 * WA * TA);
+  return launch(reinterpret_cast<const void*>(&i8_tiled<DT, WA, WB, TA, TB>), dim3(static_cast<unsigned>(tiles)),
+                dim3(64 * WA * WB), args, s);
+}
+
 template <int DT>
 int launch_product_t(const Product& p, hipStream_t s) {
+  const int64_t big = ceil_div(p.M, 256) * ceil_div(p.N, 256);
+  if (p.M > 64 && big >= 192) return launch_tiled<DT, 2, 4, 8, 4>(p, s);
+  if (p.M > 64) return launch_tiled<DT, 2, 2, 4, 4>(p, s);
   if (p.M <= 16) return launch_skinny<DT, 1, 1, 4>(p, s);
   if (p.M <= 32) return launch_skinny<DT, 1, 2, 4>(p, s);
   return launch_skinny<DT, 2, 4, 2>(p, s);
