@@ -85,6 +85,25 @@ int fp6_int8_quantize_tokens(int dtype, const void* X, int64_t ldx, int64_t M, i
 int fp6_int8_linear(const void* Xq, const void* sx, const void* Wq, const void* sw, const void* bias,
                     int dtype, void* Y, int64_t M, int64_t N, int64_t Kp, void* stream);
 
+/*
+ * fp6_int8_linear_plan -- fp6_int8_linear with the kernel forced (tuning and
+ * tests).  variant: 0 = automatic, else
+ *    1  16 channels x 16 tokens per workgroup, 4 waves split K
+ *    2  16 x 16, one wave
+ *    3  16 x 32, 4 waves split K
+ *    4  32 x 32, 4 waves split K
+ *    5  32 x 64, 4 waves split K
+ *    6  64 x 64, 4 waves share the tile
+ *    7  64 x 128, 8 waves
+ *    8  128 x 128, 8 waves
+ *    9  128 x 256, 8 waves
+ *   10  256 x 256, 8 waves
+ * Every variant handles every size and gives the same bits.
+ * Errors: as fp6_int8_linear, plus FP6_E_VALUE for an unknown variant.
+ */
+int fp6_int8_linear_plan(const void* Xq, const void* sx, const void* Wq, const void* sw, const void* bias,
+                         int dtype, void* Y, int64_t M, int64_t N, int64_t Kp, int variant, void* stream);
+
 /* Bytes of the workspace of fp6_int8_linear_tokens (the codes and scales of X),
  * 0 if M or K is outside the limits (or M is 0). */
 size_t fp6_int8_workspace_bytes(int64_t M, int64_t K);

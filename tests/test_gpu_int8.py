@@ -97,7 +97,7 @@ def test_quantize_leaves_what_is_behind_its_outputs():
 SHAPES = [(1, 1, 16), (1, 16, 64), (1, 250, 1024), (2, 17, 48), (4, 4096, 2064), (15, 63, 272), (16, 33, 4096),
           (16, 5000, 512), (17, 20, 80), (31, 129, 1040), (32, 64, 2048), (33, 16, 16), (64, 200, 640), (65, 31, 336),
           (100, 3, 96), (128, 260, 1152), (200, 511, 784), (257, 300, 4112), (300, 1030, 256), (513, 258, 128),
-          (1000, 770, 1312), (16, 16, 131056), (130, 17, 16400)]
+          (1000, 770, 1312), (2000, 2100, 400), (40, 12000, 528), (16, 16, 131056), (130, 17, 16400)]
 
 
 @pytest.mark.parametrize("out,use_bias", [("fp16", False), ("bf16", True)])
@@ -113,6 +113,29 @@ def test_linear_codes(M, N, Kp, out, use_bias):
     assert Y.shape == (M, N) and Y.dtype == DT[out]
     err = np.abs(_f64(Y) - ref)
     assert (err <= bound).all(), (err / bound).max()
+
+
+@pytest.mark.parametrize("variant", range(1, 11))
+@pytest.mark.parametrize("M,N,Kp", [(1, 1, 16), (1, 40, 2064), (17, 100, 64), (65, 31, 336), (130, 600, 4112),
+                                    (257, 513, 2000), (300, 1032, 256), (513, 264, 128), (64, 64, 1024), (33, 72, 12304)])
+def test_linear_every_variant(variant, M, N, Kp):
+    # Scales are powers of two, so the only rounding is the last one: equal bits.
+    X, W = _codes((M, Kp), M), _codes((N, Kp), N)
+    bias = torch.randint(-8, 9, (N,), generator=torch.Generator().manual_seed(1)).half()
+    Y = fp6.int8_linear_plan(X.to(DEV), W.to(DEV), torch.full((N,), 2.0 ** -8, device=DEV), torch.full((M,), 2.0 ** -4, device=DEV),
+                             variant, bias=bias.to(DEV))
+    p = X.double() @ W.double().t() * 2.0 ** -12
+    exact = p.to(torch.float32).double() == p          # the sum fits fp32: no rounding before the bias
+    assert exact.all()
+    want = (p.float() + bias.float()).half()
+    assert torch.equal(Y.cpu().view(torch.int16), want.view(torch.int16))
+
+
+def test_linear_plan_refuses_unknown_variants():
+    X, W = _codes((4, 64), 1).to(DEV), _codes((8, 64), 2).to(DEV)
+    for v in (-1, 11):
+        with pytest.raises(fp6.FP6Error, match="FP6_E_VALUE"):
+            fp6.int8_linear_plan(X, W, torch.ones(8, device=DEV), torch.ones(4, device=DEV), v)
 
 
 def test_linear_largest_sum():

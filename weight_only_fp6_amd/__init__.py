@@ -49,6 +49,7 @@ EXPORTED = (
     "fpx_linear", "fpx_linear_plan", "fpx_dequant", "fp6s_packed_bytes", "fp6s_prune_quantize",
     "fp6s_prepack", "fp6s_linear", "fp6s_linear_plan", "fp6s_linear_plan_query", "fp6s_dequant",
     "fp6_int8_padded_k", "fp6_int8_quantize_rows", "fp6_int8_quantize_tokens", "fp6_int8_linear",
+    "fp6_int8_linear_plan",
     "fp6_int8_workspace_bytes", "fp6_int8_linear_tokens", "fpx_moe_workspace_bytes", "fpx_moe_experts",
     "fpx_moe_layer",
 )
@@ -106,6 +107,7 @@ def _load() -> ctypes.CDLL:
         "fp6_int8_quantize_rows": ([vp, i64, i64, vp, vp], i32),
         "fp6_int8_quantize_tokens": ([i32, vp, i64, i64, i64, vp, vp, vp], i32),
         "fp6_int8_linear": ([vp, vp, vp, vp, vp, i32, vp, i64, i64, i64, vp], i32),
+        "fp6_int8_linear_plan": ([vp, vp, vp, vp, vp, i32, vp, i64, i64, i64, i32, vp], i32),
         "fp6_int8_workspace_bytes": ([i64, i64], sz),
         "fp6_int8_linear_tokens": ([i32, vp, i64, vp, vp, vp, i32, vp, i64, i64, i64, vp, sz, vp], i32),
         "fpx_moe_workspace_bytes": ([i64, i64, i64, i64, i64], sz),
@@ -520,6 +522,28 @@ def int8_linear(X, W, w_scales, x_scales=None, bias=None, out=None, out_dtype=No
             ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
             st = _lib.fp6_int8_linear_tokens(dt, px, ldx, pw, psw, pb, od, py, M, N, K, ws.data_ptr(), nbytes, s)
         _check("fp6_int8_linear" if codes else "fp6_int8_linear_tokens", st)
+    return out
+
+
+def int8_linear_plan(X, W, w_scales, x_scales, variant: int, bias=None, out=None, out_dtype=None, stream=None):
+    """:func:`int8_linear` of int8 codes with the kernel forced (see ``fp6_int8_linear_plan``)."""
+    import torch
+    if not isinstance(X, torch.Tensor) or X.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("X must be an int8 [M,Kp] and W an int8 [N,Kp] tensor")
+    (M, kp), N, dev = X.shape, W.shape[0], X.device
+    dtype = out.dtype if out is not None else out_dtype or torch.float16
+    _need(dtype in (torch.float16, torch.bfloat16), "the output is fp16 or bf16")
+    px, pw = _gpu_tensor(X, torch.int8, (M, kp), None, "X"), _gpu_tensor(W, torch.int8, (N, kp), dev, "W")
+    psx = _gpu_tensor(x_scales, torch.float32, (M,), dev, "x_scales")
+    psw = _gpu_tensor(w_scales, torch.float32, (N,), dev, "w_scales")
+    pb = 0 if bias is None else _gpu_tensor(bias, dtype, (N,), dev, "bias")
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.empty((M, N), dtype=dtype, device=dev)
+        py = _gpu_tensor(out, dtype, (M, N), dev, "out")
+        _check("fp6_int8_linear_plan",
+               _lib.fp6_int8_linear_plan(px, psx, pw, psw, pb, 0 if dtype == torch.float16 else 1, py, M, N, kp,
+                                         variant, s))
     return out
 
 

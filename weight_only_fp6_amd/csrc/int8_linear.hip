@@ -13,6 +13,7 @@
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float float4v __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -188,129 +189,32 @@ __device__ __forceinline__ void store_tile(void* __restrict__ Y, const i32x4 (&a
 }
 
 // ---------------------------------------------------------------------------
-// Skinny product (few tokens): a workgroup of 8 waves owns 16*RB channels and
-// 16*MB tokens; its waves split K in interleaved chunks of 64*S bytes, read
-// both operands straight into MFMA fragments (lane (r, g): 16*S contiguous
-// bytes of row r at offset 16*S*g of the chunk; both operands take k in the
-// same order, so any order is right) and add their exact integer partial sums
-// through LDS.
-// ---------------------------------------------------------------------------
-template <int DT, int RB, int MB, int S>
-__global__ __launch_bounds__(512) void i8_skinny(const int8_t* __restrict__ Xq, const float* __restrict__ sx,
-                                                 const int8_t* __restrict__ Wq, const float* __restrict__ sw,
-                                                 const void* __restrict__ bias, void* __restrict__ Y,
-                                                 int64_t M, int64_t N, int64_t kp) {
-  constexpr int kWaves = 8, kAcc = RB * MB;
-  __shared__ i32x4 red[kWaves][kAcc][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = lane & 15, g = lane >> 4;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16 * RB;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 16 * MB;
-  const int chunks = static_cast<int>((kp + 64 * S - 1) / (64 * S));
-  const int8_t* w[RB];
-  const int8_t* x[MB];
-#pragma unroll
-  for (int a = 0; a < RB; ++a) {
-    const int64_t n = n0 + 16 * a + r;
-    w[a] = Wq + (n < N ? n : N - 1) * kp;
-  }
-#pragma unroll
-  for (int b = 0; b < MB; ++b) {
-    const int64_t m = m0 + 16 * b + r;
-    x[b] = Xq + (m < M ? m : M - 1) * kp;
-  }
-  i32x4 acc[RB][MB] = {};
-  i32x4 wf[2][RB][S], xf[2][MB][S];
-  auto load = [&](int slot, int c) {
-    const int64_t k0 = static_cast<int64_t>(c) * 64 * S + 16 * S * g;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int64_t k = k0 + 16 * s;
-      const bool in = k < kp;
-      const int64_t kk = in ? k : 0;  // a unit behind the row: a stand-in, times zero
-#pragma unroll
-      for (int a = 0; a < RB; ++a) wf[slot][a][s] = *reinterpret_cast<const i32x4*>(w[a] + kk);
-#pragma unroll
-      for (int b = 0; b < MB; ++b) {
-        const i32x4 v = *reinterpret_cast<const i32x4*>(x[b] + kk);
-        xf[slot][b][s] = in ? v : i32x4{0, 0, 0, 0};
-      }
-    }
-  };
-  auto mul = [&](int slot) {
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-      for (int a = 0; a < RB; ++a)
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-          acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[slot][a][s], xf[slot][b][s], acc[a][b], 0, 0, 0);
-  };
-  int c = wave;
-  if (c < chunks) {
-    load(0, c);
-    for (;;) {
-      const int c1 = c + kWaves;
-      if (c1 >= chunks) {
-        mul(0);
-        break;
-      }
-      load(1, c1);
-      mul(0);
-      const int c2 = c1 + kWaves;
-      if (c2 >= chunks) {
-        mul(1);
-        break;
-      }
-      load(0, c2);
-      mul(1);
-      c = c2;
-    }
-  }
-#pragma unroll
-  for (int a = 0; a < RB; ++a)
-#pragma unroll
-    for (int b = 0; b < MB; ++b) red[wave][a * MB + b][lane] = acc[a][b];
-  __syncthreads();
-  for (int i = wave; i < kAcc; i += kWaves) {
-    i32x4 sum = red[0][i][lane];
-#pragma unroll
-    for (int v = 1; v < kWaves; ++v) sum += red[v][i][lane];
-    const int a = i / MB, b = i % MB;
-    const int64_t m = m0 + 16 * b + r, n = n0 + 16 * a + 4 * g;
-    const i32x4 one[1][1] = {{sum}};
-    if ((N & 3) == 0 && m < M && n < N) {
-      store_tile<DT, 1, 1, true>(Y, one, sx, sw, bias, m, n, M, N);
-    } else {
-      store_tile<DT, 1, 1, false>(Y, one, sx, sw, bias, m, n, M, N);
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Tiled product (many tokens).  A workgroup of WA x WB waves owns a tile of
-// 16*WA*TA channels x 16*WB*TB tokens, a wave 16*TA x 16*TB of it.  K runs in
-// steps of 64 bytes through a ring of four LDS stages, filled by direct LDS
-// loads.  Step t multiplies fragments that are in registers, reads those of
-// step t+1 from LDS between the MFMAs, and requests step t+3 into the stage
-// that step t-1 left; one barrier per step, and a load has two steps to arrive.
-// Each stage is its own LDS array and the barrier carries no fence, so that
-// nothing waits for more loads than the next step needs.
+// Product.  A workgroup of WA x WB waves owns a tile of 16*WA*TA channels x
+// 16*WB*TB tokens, a wave 16*TA x 16*TB of it; with WK > 1 (few tokens), WK
+// waves own the whole tile, each with a ring of its own and a part of K, and
+// add their exact sums through LDS.  K runs in
+// steps of 128 bytes (a cache line of every row: with steps of 64, the first
+// form, each line came twice from the L2) through a ring of D LDS stages filled
+// by direct LDS loads.  A step is two halves of 64 bytes; the fragments of a
+// half are read from LDS between the MFMAs of the half before it.  One barrier
+// per step, before its second half: every wave waits there until its reads of the
+// stage's last fragments are done, so step t+D may be requested into it, and
+// until its loads of step t+1 have landed; a load has D-1 steps to arrive.  Each stage is its own LDS array
+// and the barrier carries no fence, so that nothing waits for more loads than
+// the next step needs.
 //
-// An LDS row is 64 bytes in four 16-byte units; unit c of row r lies at place
-// (c + r/2) % 4, so that 8 rows' fragment reads of one c cover 8 different
-// places of a 128-byte line.  The direct loads are linear on the LDS side, so
-// the turn is made on the global side.  Units behind a row's end (Kp need not
-// be a multiple of 64) are loaded from 16 bytes of zeros; rows behind the last
-// repeat it and are not stored.
+// Unit c (16 bytes) of LDS row r lies at place c ^ (r % 8), so that the eight
+// rows of a quarter wave's fragment read cover the eight places of a line.  The
+// direct loads are linear on the LDS side, so the turn is made on the global
+// side.  Kp need not be a multiple of 128: the last units of the ring are filled
+// with zeros.  Rows behind the last repeat it and are not stored.
 // ---------------------------------------------------------------------------
-__device__ const u32x4 kZeroUnit[1] = {};
-
 __device__ __forceinline__ void barrier_no_fence() { asm volatile("s_barrier" ::: "memory"); }
 
+// Until at most N of the wave's loads are in flight and its LDS reads are done.
 template <int N>
-__device__ __forceinline__ void wait_loads() {  // until at most N of the wave's loads are in flight
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
 
 // Workgroup index -> tile, XCD-aware: workgroups go to the 8 XCDs in turn, and
@@ -327,16 +231,26 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t mt, uint32_t nt, ui
   tm = band * kBand + (in - tn * rows);
 }
 
-template <int DT, int WA, int WB, int TA, int TB>
-__global__ __launch_bounds__(64 * WA * WB) void i8_tiled(const int8_t* __restrict__ Xq, const float* __restrict__ sx,
+//
+// The second launch bound keeps the accumulators of the 4-wave forms in vector
+// registers; with more room the compiler moves them to and from the
+// accumulation registers in every step.
+template <int DT, int WA, int WB, int TA, int TB, int D, int WK, bool NT>
+__global__ __launch_bounds__(64 * WA * WB * WK, 2) void i8_tiled(const int8_t* __restrict__ Xq, const float* __restrict__ sx,
                                                          const int8_t* __restrict__ Wq, const float* __restrict__ sw,
                                                          const void* __restrict__ bias, void* __restrict__ Y,
                                                          int64_t M, int64_t N, int64_t kp) {
   constexpr int kThreads = 64 * WA * WB, kRowsA = 16 * WA * TA, kRowsB = 16 * WB * TB;
-  constexpr int kUnits = (kRowsA + kRowsB) * 4, kLoads = kUnits / kThreads;
-  static_assert(kUnits % kThreads == 0, "every thread makes the same number of loads");
-  __shared__ i32x4 st0[kUnits], st1[kUnits], st2[kUnits], st3[kUnits];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int kUnits = (kRowsA + kRowsB) * 8, kLoads = kUnits / kThreads;
+  static_assert(kUnits % kThreads == 0 && kRowsA * 8 % kThreads == 0, "a load of the workgroup reads one operand");
+  static_assert(D == 2 || D == 4, "ring depths");
+  static_assert(WK == 1 || WA * WB == 1, "waves share a ring or split K, not both");
+  constexpr bool kShared = WA * WB > 1;  // a ring of several waves: barriers
+  __shared__ i32x4 st0[WK * kUnits], st1[WK * kUnits], st2[D > 2 ? WK * kUnits : 1], st3[D > 2 ? WK * kUnits : 1];
+  const int wk = kShared ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  i32x4* const ring[4] = {st0 + wk * kUnits, st1 + wk * kUnits, st2 + (D > 2 ? wk * kUnits : 0),
+                          st3 + (D > 2 ? wk * kUnits : 0)};
+  const int tid = kShared ? threadIdx.x : threadIdx.x & 63, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, g = lane >> 4;
   const int wa = wave / WB, wb = wave - wa * WB;
   uint32_t tm, tn;
@@ -344,95 +258,211 @@ __global__ __launch_bounds__(64 * WA * WB) void i8_tiled(const int8_t* __restric
           tm, tn);
   const int64_t n0 = static_cast<int64_t>(tn) * kRowsA, m0 = static_cast<int64_t>(tm) * kRowsB;
 
-  // This thread's units of a stage: place p of row p/4 holds unit (p - row/2) % 4.
-  const int8_t* src[kLoads];
-  int unit[kLoads];
+  // The scales and biases of the tile, for the epilogue.
+  __shared__ float s_sx[kRowsB], s_sw[kRowsA], s_bias[kRowsA];
+  if constexpr (WK == 1) {
+    for (int i = threadIdx.x; i < kRowsA; i += kThreads) {
+      const int64_t n = n0 + i < N ? n0 + i : N - 1;
+      s_sw[i] = sw[n];
+      s_bias[i] = bias ? static_cast<float>(static_cast<const typename Elem<DT>::T*>(bias)[n]) : 0.0f;
+    }
+    for (int i = threadIdx.x; i < kRowsB; i += kThreads) s_sx[i] = sx[m0 + i < M ? m0 + i : M - 1];
+  }
+
+  // This thread's units of a stage: place p of LDS row `row` holds unit p ^ (row % 8).
+  // Addresses are a wave-uniform base and a 32-bit offset inside the tile's
+  // rows (at most 256 * 131056).
+  const int8_t* base_a = Wq + n0 * kp;
+  const int8_t* base_b = Xq + m0 * kp;
+  uint32_t off[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int p = i * kThreads + tid, row = p >> 2;
-    unit[i] = ((p & 3) - (row >> 1)) & 3;
-    if (row < kRowsA) {
-      const int64_t n = n0 + row < N ? n0 + row : N - 1;
-      src[i] = Wq + n * kp + 16 * unit[i];
-    } else {
-      const int64_t m = m0 + row - kRowsA < M ? m0 + row - kRowsA : M - 1;
-      src[i] = Xq + m * kp + 16 * unit[i];
-    }
+    const int p = i * kThreads + tid, row = p >> 3, unit = (p ^ row) & 7;
+    const bool in_a = row < kRowsA;
+    const int64_t left = in_a ? N - n0 : M - m0;  // rows of the tile that exist
+    const int rr = in_a ? row : row - kRowsA;
+    off[i] = static_cast<uint32_t>(rr < left ? rr : left - 1) * static_cast<uint32_t>(kp) + 16 * unit;
   }
-  const int steps = static_cast<int>((kp + 63) >> 6);
-  const int tail_units = static_cast<int>(kp - (static_cast<int64_t>(steps - 1) << 6)) >> 4;  // 1..4
-  auto request = [&](i32x4* stage, int t) {
-    const int tt = t < steps ? t : steps - 1;  // behind the end: the last step again, never read
-    const bool tail = tt == steps - 1;
+  // Steps t0 .. t1-1 are this wave's (WK > 1: its part of K), those below
+  // `full` are whole lines; behind t1 the ring is filled with zeros.
+  const int total = static_cast<int>((kp + 127) >> 7);
+  const int t0 = WK == 1 ? 0 : wk * total / WK, t1 = WK == 1 ? total : (wk + 1) * total / WK;
+  const int full = t1 < static_cast<int>(kp >> 7) ? t1 : static_cast<int>(kp >> 7);
+  const int t_end = t0 + (t1 - t0 + D - 1) / D * D;  // the last round's end
+  const int uwave = __builtin_amdgcn_readfirstlane(wave);
+  auto load_unit = [&](i32x4* stage, const int8_t* a, const int8_t* b, int i) {
+    auto* dst = reinterpret_cast<__attribute__((address_space(3))) void*>(
+        reinterpret_cast<uintptr_t>(stage + i * kThreads + uwave * 64));
+    constexpr int kNonTemporal = 2;
+    if (i * kThreads < kRowsA * 8)
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(a + off[i]), dst, 16, 0, NT ? kNonTemporal : 0);
+    else
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(b + off[i]), dst, 16, 0, 0);
+  };
+  // The same for any step: the row's last, partial step and the zeros behind it
+  // go through registers.  Nothing is in flight afterwards, so the next waits
+  // find less than they allow for and nothing early.
+  auto request_any = [&](i32x4* stage, int t) {
+    const int64_t k = static_cast<int64_t>(t) * 128;
+    if (t < full) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load_unit(stage, base_a + k, base_b + k, i);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int8_t* from = src[i] + static_cast<int64_t>(tt) * 64;
-      if (tail && unit[i] >= tail_units) from = reinterpret_cast<const int8_t*>(&kZeroUnit[0]);
-      __builtin_amdgcn_global_load_lds(
-          static_cast<const void*>(from),
-          reinterpret_cast<__attribute__((address_space(3))) void*>(
-              reinterpret_cast<uintptr_t>(stage + i * kThreads + wave * 64)),
-          16, 0, 0);
+      const int p = i * kThreads + tid, unit = (p ^ (p >> 3)) & 7;
+      i32x4 v = {0, 0, 0, 0};
+      if (t < t1 && k + 16 * unit < kp)
+        v = *reinterpret_cast<const i32x4*>((i * kThreads < kRowsA * 8 ? base_a : base_b) + k + off[i]);
+      stage[p] = v;
+      asm volatile("" ::: "memory");  // one at a time: these are few, and registers are short
     }
+    __builtin_amdgcn_s_waitcnt(0);
   };
-  const int place = (g + (r >> 1)) & 3;  // 16-row blocks start at multiples of 4 half-rows
-  const int at_a = (wa * TA * 16 + r) * 4 + place, at_b = (kRowsA + wb * TB * 16 + r) * 4 + place;
-  i32x4 fa[2][TA], fb[2][TB], acc[TA][TB] = {};
-  auto read = [&](const i32x4* stage, i32x4 (&a)[TA], i32x4 (&b)[TB]) {
-#pragma unroll
-    for (int j = 0; j < TB; ++j) b[j] = stage[at_b + 64 * j];
-#pragma unroll
-    for (int i = 0; i < TA; ++i) a[i] = stage[at_a + 64 * i];
+  const int row_a = (wa * TA * 16 + r) * 8, row_b = (kRowsA + wb * TB * 16 + r) * 8;  // rows 16 i + r: i * 128 units on
+  const int place[2] = {g ^ (r & 7), (4 + g) ^ (r & 7)};
+  i32x4 fa[TA], fb[2][TB], acc[TA][TB] = {};
+  auto mul = [&](int i, const i32x4 (&b)[TB], int j) {
+    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[i], b[j], acc[i][j], 0, 0, 0);
   };
-  auto step = [&](int t, i32x4* next, i32x4* free_stage, auto P) {
-    constexpr int p = decltype(P)::value;
-    wait_loads<kLoads>();
-    barrier_no_fence();
-    request(free_stage, t + 3);
-    __builtin_amdgcn_sched_barrier(0);
-    read(next, fa[1 - p], fb[1 - p]);
+  // The MFMAs of half H with the reads of the half that follows (half `to` of
+  // `next`) and, with LOAD, the loads of a later step into `dst`, all spread
+  // among them: a wave issues in order, and loads issued in one go would hold
+  // its MFMAs back until the address unit has taken them (16 cycles each at
+  // 64 bytes per cycle).  Channel fragment i is read as soon as this half is
+  // done with it, into the same registers; the token fragments are
+  // double-buffered.
+  auto half = [&](auto H, const i32x4* next, auto LOAD, i32x4* dst, const int8_t* a, const int8_t* b) {
+    constexpr int p = decltype(H)::value, to = 1 - p;
+    constexpr int kLd = decltype(LOAD)::value ? (kLoads + TA - 1) / TA : 0;  // loads per channel block
 #pragma unroll
-    for (int i = 0; i < TA; ++i)
+    for (int i = 0; i < TA; ++i) {
 #pragma unroll
-      for (int j = 0; j < TB; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[p][i], fb[p][j], acc[i][j], 0, 0, 0);
-    // MFMAs, then the one fragment read that falls to them: the wait before
-    // the first MFMA finds only the previous step's reads, long done.
-    constexpr int kReads = TA + TB, kPer = TA * TB / kReads > 0 ? TA * TB / kReads : 1;
+      for (int j = 0; j < TB / 2; ++j) mul(i, fb[p], j);
 #pragma unroll
-    for (int i = 0; i < kReads; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
+      for (int l = i * kLd; l < (i + 1) * kLd; ++l)
+        if (l < kLoads) load_unit(dst, a, b, l);
+#pragma unroll
+      for (int j = i; j < TB; j += TA) fb[to][j] = next[row_b + 128 * j + place[to]];
+#pragma unroll
+      for (int j = TB / 2; j < TB; ++j) mul(i, fb[p], j);
+      fa[i] = next[row_a + 128 * i + place[to]];
+    }
+#pragma unroll
+    for (int i = 0; i < TA; ++i) {
+      if (TB > 1) __builtin_amdgcn_sched_group_barrier(0x008, TB / 2, 0);
+      if (kLd > 0 && i * kLd < kLoads) __builtin_amdgcn_sched_group_barrier(0x010, kLd, 0);
+      if (i < TB) __builtin_amdgcn_sched_group_barrier(0x100, (TB + TA - 1) / TA, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, TB - TB / 2, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, TA * TB, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
-  request(st0, 0);
-  request(st1, 1);
-  request(st2, 2);
-  wait_loads<2 * kLoads>();
-  barrier_no_fence();
-  read(st0, fa[0], fb[0]);
-  constexpr std::integral_constant<int, 0> even{};
-  constexpr std::integral_constant<int, 1> odd{};
-  int t = 0;
-  for (; t + 4 <= steps; t += 4) {
-    step(t, st1, st3, even);
-    step(t + 1, st2, st0, odd);
-    step(t + 2, st3, st1, even);
-    step(t + 3, st0, st2, odd);
-  }
-  if (t < steps) step(t, st1, st3, even);
-  if (t + 1 < steps) step(t + 1, st2, st0, odd);
-  if (t + 2 < steps) step(t + 2, st3, st1, even);
+  constexpr std::integral_constant<int, 0> first{};
+  constexpr std::integral_constant<int, 1> second{};
+  auto step = [&](int t, auto S, auto ANY) {  // step t, (t - t0) % D == S
+    constexpr int st = decltype(S)::value;
+    half(first, ring[st], std::false_type{}, nullptr, nullptr, nullptr);
+    // Behind the last whole line fewer loads are in flight than the count allows for.
+    if (decltype(ANY)::value && t + D - 1 >= full) wait_loads<0>();
+    else wait_loads<(D - 2) * kLoads>();
+    if constexpr (kShared) barrier_no_fence();
+    if constexpr (decltype(ANY)::value) {
+      if (t + D < t_end) request_any(ring[st], t + D);
+      half(second, ring[(st + 1) % D], std::false_type{}, nullptr, nullptr, nullptr);
+    } else {
+      // Opaque scalar bases: added to the offsets by the load itself.  Left to
+      // itself the compiler keeps base + offset of every load in registers and
+      // adds k to each.
+      const int8_t* a = base_a + static_cast<int64_t>(t + D) * 128;
+      const int8_t* b = base_b + static_cast<int64_t>(t + D) * 128;
+      asm("" : "+s"(a), "+s"(b));
+      half(second, ring[(st + 1) % D], std::true_type{}, ring[st], a, b);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < D; ++i) request_any(ring[i], t0 + i);
+  wait_loads<(D - 1) * kLoads>();
+  if constexpr (kShared) barrier_no_fence();
+#pragma unroll
+  for (int j = 0; j < TB; ++j) fb[0][j] = ring[0][row_b + 128 * j + place[0]];
+#pragma unroll
+  for (int i = 0; i < TA; ++i) fa[i] = ring[0][row_a + 128 * i + place[0]];
+  auto round = [&](int t, auto ANY) {
+    step(t, std::integral_constant<int, 0>{}, ANY);
+    step(t + 1, std::integral_constant<int, 1>{}, ANY);
+    if constexpr (D > 2) {
+      step(t + 2, std::integral_constant<int, 2>{}, ANY);
+      step(t + 3, std::integral_constant<int, 3>{}, ANY);
+    }
+  };
+  int t = t0;
+  for (; t + 2 * D - 1 < full; t += D) round(t, std::false_type{});
+  for (; t < t1; t += D) round(t, std::true_type{});
   __builtin_amdgcn_s_waitcnt(0);  // no load may land after the workgroup has left
 
-  const bool whole = (N & 3) == 0 && n0 + kRowsA <= N && m0 + kRowsB <= M;
-  const int64_t nw = n0 + wa * TA * 16 + 4 * g, mw = m0 + wb * TB * 16 + r;
-  if (whole) {
-    store_tile<DT, TA, TB, true>(Y, acc, sx, sw, bias, mw, nw, M, N);
-  } else {
-    store_tile<DT, TA, TB, false>(Y, acc, sx, sw, bias, mw, nw, M, N);
+  if constexpr (WK > 1) {
+    // The waves' sums meet in LDS (exact, so in any order); wave i takes block i, i + WK, ...
+    __shared__ i32x4 red[WK][TA * TB][64];
+#pragma unroll
+    for (int i = 0; i < TA * TB; ++i) red[wk][i][lane] = acc[i / TB][i % TB];
+    __syncthreads();
+    for (int i = wk; i < TA * TB; i += WK) {
+      i32x4 sum[1][1] = {{red[0][i][lane]}};
+#pragma unroll
+      for (int w = 1; w < WK; ++w) sum[0][0] += red[w][i][lane];
+      const int64_t n = n0 + 16 * (i / TB) + 4 * g, m = m0 + 16 * (i % TB) + r;
+      if ((N & 3) == 0 && m < M && n < N) store_tile<DT, 1, 1, true>(Y, sum, sx, sw, bias, m, n, M, N);
+      else store_tile<DT, 1, 1, false>(Y, sum, sx, sw, bias, m, n, M, N);
+    }
+    return;
+  }
+  // Epilogue.  A wave scales its block into its own part of the ring (free
+  // after the barrier), a token's channels side by side, and stores whole rows
+  // of it, 16 bytes per lane: stored straight from the accumulators, a
+  // request would touch 16 rows with 32 bytes each.
+  using T = typename Elem<DT>::T;
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  constexpr int kCols = 16 * TA, kPitch = kCols + 8;  // 16 bytes more: rows start at different banks
+  constexpr int kRowsOut = 16 * TB;
+  static_assert(kPitch * 2 * 16 <= kUnits * 16 / (WA * WB), "16 tokens of every wave fit one stage");
+  const int64_t nw = n0 + wa * kCols, mw = m0 + wb * kRowsOut;
+  if constexpr (kShared) __syncthreads();
+  T* buf = reinterpret_cast<T*>(st0 + wave * (kUnits / (WA * WB)));
+  const T* bv = static_cast<const T*>(bias);
+  const bool vec = (N & 7) == 0;
+#pragma unroll
+  for (int j = 0; j < TB; ++j) {
+    const float xs = s_sx[wb * kRowsOut + 16 * j + r];
+#pragma unroll
+    for (int i = 0; i < TA; ++i) {
+      const float4v ws = *reinterpret_cast<const float4v*>(&s_sw[wa * kCols + 16 * i + 4 * g]);
+      const float4v bs = *reinterpret_cast<const float4v*>(&s_bias[wa * kCols + 16 * i + 4 * g]);
+      T4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = static_cast<T>((static_cast<float>(acc[i][j][e]) * ws[e]) * xs + bs[e]);
+      *reinterpret_cast<T4*>(&buf[r * kPitch + 16 * i + 4 * g]) = o;
+    }
+    __builtin_amdgcn_wave_barrier();
+    constexpr int kUnitsRow = kCols / 8;
+#pragma unroll
+    for (int u0 = 0; u0 < 16 * kUnitsRow; u0 += 64) {
+      const int u = u0 + lane, row = u / kUnitsRow, col = (u % kUnitsRow) * 8;
+      const int64_t m = mw + 16 * j + row, n = nw + col;
+      if (u < 16 * kUnitsRow && m < M && n < N) {
+        T* y = static_cast<T*>(Y) + m * N + n;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(&buf[row * kPitch + col]);
+        if (vec && n + 8 <= N) {
+          *reinterpret_cast<u32x4*>(y) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < N) y[e] = buf[row * kPitch + col + e];
+        }
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -476,52 +506,112 @@ struct Product {
   int64_t M, N, kp;
 };
 
-template <int DT, int RB, int MB, int S>
-int launch_skinny(const Product& p, hipStream_t s) {
+// Weights of at least this size, read once per call, are loaded with the
+// non-temporal hint: 16x28672x8192 46 -> 42 us, 1x28672x8192 42 -> 37 us.
+// Smaller ones may still be in the 256 MB cache from the call before
+// (16x4096x4096 7.3 us from there, 9.7 us with the hint).
+constexpr int64_t kStreamBytes = int64_t(64) << 20;
+
+template <int DT, int WA, int WB, int TA, int TB, int D, int WK = 1>
+int launch_tiled(const Product& p, hipStream_t s) {
   const int8_t *x = static_cast<const int8_t*>(p.xq), *w = static_cast<const int8_t*>(p.wq);
   const float *sx = static_cast<const float*>(p.sx), *sw = static_cast<const float*>(p.sw);
   const void* bias = p.bias;
-  // The grid's second dimension holds at most 65535 groups of tokens.
-  const int64_t per = int64_t(65535) * 16 * MB;
+  // The grid (tiles times threads below 2^32) takes this many token tiles at once.
+  constexpr int64_t kTileM = 16 * WB * TB, kTileN = 16 * WA * TA, kThreads = 64 * WA * WB * WK;
+  const int64_t per = ((int64_t(1) << 31) / kThreads) / ceil_div(p.N, kTileN) * kTileM;
   for (int64_t m0 = 0; m0 < p.M; m0 += per) {
     int64_t M = p.M - m0 < per ? p.M - m0 : per, N = p.N, kp = p.kp;
     const int8_t* xm = x + m0 * kp;
     const float* sxm = sx + m0;
     void* y = static_cast<uint16_t*>(p.y) + m0 * N;
     void* args[] = {&xm, &sxm, &w, &sw, &bias, &y, &M, &N, &kp};
-    const dim3 grid(static_cast<unsigned>(ceil_div(N, 16 * RB)), static_cast<unsigned>(ceil_div(M, 16 * MB)));
-    const int st = launch(reinterpret_cast<const void*>(&i8_skinny<DT, RB, MB, S>), grid, dim3(512), args, s);
+    const dim3 grid(static_cast<unsigned>(ceil_div(M, kTileM) * ceil_div(N, kTileN)));
+    const bool nt = M <= kTileM && N * kp >= kStreamBytes;
+    const void* kern = nt ? reinterpret_cast<const void*>(&i8_tiled<DT, WA, WB, TA, TB, D, WK, true>)
+                          : reinterpret_cast<const void*>(&i8_tiled<DT, WA, WB, TA, TB, D, WK, false>);
+    const int st = launch(kern, grid, dim3(kThreads), args, s);
     if (st != FP6_OK) return st;
   }
   return FP6_OK;
 }
 
-template <int DT, int WA, int WB, int TA, int TB>
-int launch_tiled(const Product& p, hipStream_t s) {
-  const int8_t *x = static_cast<const int8_t*>(p.xq), *w = static_cast<const int8_t*>(p.wq);
-  const float *sx = static_cast<const float*>(p.sx), *sw = static_cast<const float*>(p.sw);
-  const void* bias = p.bias;
-  void* y = p.y;
-  int64_t M = p.M, N = p.N, kp = p.kp;
-  void* args[] = {&x, &sx, &w, &sw, &bias, &y, &M, &N, &kp};
-  // At most 2^36 / 2^12 tiles of 64 * 64 or more, under 2^32 threads in all... 
-  const int64_t tiles = ceil_div(M, 16 * WB * TB) * ceil_div(N, 16 * WA * TA);
-  return launch(reinterpret_cast<const void*>(&i8_tiled<DT, WA, WB, TA, TB>), dim3(static_cast<unsigned>(tiles)),
-                dim3(64 * WA * WB), args, s);
+// Kernel configurations of fp6_int8_linear_plan: channels x tokens per workgroup.
+enum Variant : int {
+  kAuto, kSplit16x16, kOne16x16, kSplit16x32, kSplit32x32, kSplit32x64,
+  kTile64x64, kTile64x128, kTile128x128, kTile128x256, kTile256x256, kNumVariants
+};
+
+// The tiled forms' cost on a shape: rounds of workgroups over the CUs, each
+// round as long as a full one was measured, the last, partial one between a
+// nearly empty and a full one by its fill (us at K = 4096; the form's tile,
+// workgroups per CU).  Every cost grows with K alike.
+struct TileCost {
+  int variant, n, m, per_cu;
+  float empty, full;
+};
+constexpr TileCost kTiles[] = {
+    {kTile64x64, 64, 64, 2, 8.9f, 14.5f},     {kTile64x128, 64, 128, 1, 11.1f, 13.4f},
+    {kTile128x128, 128, 128, 1, 15.3f, 20.3f}, {kTile128x256, 128, 256, 1, 26.5f, 35.7f},
+    {kTile256x256, 256, 256, 1, 41.0f, 60.0f},
+};
+
+int choose_variant(const Product& p, int cus) {
+  const int64_t nb = ceil_div(p.N, 16);
+  // Up to 16 tokens: four waves that split K while that is at most two
+  // workgroups per CU (16x4096x4096 6.0 us against 7.2 with one wave,
+  // 16x4096x11008 13.0 against 20.8), else one wave per workgroup
+  // (16x11008x4096 13.1 against 14.3).
+  if (p.M <= 16) return nb <= 2 * cus ? kSplit16x16 : kOne16x16;
+  // The forms whose waves split K run one workgroup per CU; the smallest one
+  // that needs no second round (32x4096x4096 5.8 us against 8.8 with 64x64
+  // tiles, 64x8192x8192 17.0 against 24.3, 128x4096x11008 23.4 against 30.1;
+  // where it needs one: 64x11008x4096 20.9 against 15.2).
+  if (ceil_div(p.M, 32) * nb <= cus) return kSplit16x32;
+  if (ceil_div(p.M, 32) * ceil_div(nb, 2) <= cus) return kSplit32x32;
+  if (ceil_div(p.M, 64) * ceil_div(nb, 2) <= cus) return kSplit32x64;
+  int best = kTile64x64;
+  float best_cost = 0.0f;
+  for (const TileCost& t : kTiles) {
+    const float rounds = static_cast<float>(ceil_div(p.M, t.m) * ceil_div(p.N, t.n)) / static_cast<float>(cus * t.per_cu);
+    const float whole = static_cast<float>(static_cast<int64_t>(rounds)), part = rounds - whole;
+    const float cost = whole * t.full + (part > 0.0f ? t.empty + (t.full - t.empty) * part : 0.0f);
+    if (best_cost == 0.0f || cost < best_cost) {
+      best = t.variant;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+int device_cus() {
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+    cus = 256;
+  return cus;
 }
 
 template <int DT>
-int launch_product_t(const Product& p, hipStream_t s) {
-  const int64_t big = ceil_div(p.M, 256) * ceil_div(p.N, 256);
-  if (p.M > 64 && big >= 192) return launch_tiled<DT, 2, 4, 8, 4>(p, s);
-  if (p.M > 64) return launch_tiled<DT, 2, 2, 4, 4>(p, s);
-  if (p.M <= 16) return launch_skinny<DT, 1, 1, 4>(p, s);
-  if (p.M <= 32) return launch_skinny<DT, 1, 2, 4>(p, s);
-  return launch_skinny<DT, 2, 4, 2>(p, s);
+int launch_product_t(const Product& p, int variant, hipStream_t s) {
+  switch (variant) {  // WA, WB, TA, TB, D, WK
+    case kSplit16x16: return launch_tiled<DT, 1, 1, 1, 1, 4, 4>(p, s);
+    case kOne16x16: return launch_tiled<DT, 1, 1, 1, 1, 4>(p, s);
+    case kSplit16x32: return launch_tiled<DT, 1, 1, 1, 2, 4, 4>(p, s);
+    case kSplit32x32: return launch_tiled<DT, 1, 1, 2, 2, 4, 4>(p, s);
+    case kSplit32x64: return launch_tiled<DT, 1, 1, 2, 4, 2, 4>(p, s);
+    case kTile64x64: return launch_tiled<DT, 2, 2, 2, 2, 4>(p, s);
+    case kTile64x128: return launch_tiled<DT, 2, 4, 2, 2, 4>(p, s);
+    case kTile128x128: return launch_tiled<DT, 2, 4, 4, 2, 4>(p, s);
+    case kTile128x256: return launch_tiled<DT, 2, 4, 4, 4, 2>(p, s);
+    case kTile256x256: return launch_tiled<DT, 2, 4, 8, 4, 2>(p, s);
+    default: return FP6_E_VALUE;
+  }
 }
 
-int launch_product(int dtype, const Product& p, hipStream_t s) {
-  return dtype == FP6_FP16 ? launch_product_t<FP6_FP16>(p, s) : launch_product_t<FP6_BF16>(p, s);
+int launch_product(int dtype, const Product& p, int variant, hipStream_t s) {
+  if (variant == kAuto) variant = choose_variant(p, device_cus());
+  return dtype == FP6_FP16 ? launch_product_t<FP6_FP16>(p, variant, s) : launch_product_t<FP6_BF16>(p, variant, s);
 }
 
 bool sizes_ok(int64_t M, int64_t N, int64_t kp) {
@@ -544,16 +634,21 @@ int fp6_int8_quantize_tokens(int dtype, const void* X, int64_t ldx, int64_t M, i
   return launch_quantize(dtype, X, ldx, M, K, Xq, scales, static_cast<hipStream_t>(stream));
 }
 
-int fp6_int8_linear(const void* Xq, const void* sx, const void* Wq, const void* sw, const void* bias, int dtype,
-                    void* Y, int64_t M, int64_t N, int64_t Kp, void* stream) {
-  if (!dtype_ok(dtype)) return FP6_E_VALUE;
+int fp6_int8_linear_plan(const void* Xq, const void* sx, const void* Wq, const void* sw, const void* bias, int dtype,
+                         void* Y, int64_t M, int64_t N, int64_t Kp, int variant, void* stream) {
+  if (!dtype_ok(dtype) || variant < 0 || variant >= kNumVariants) return FP6_E_VALUE;
   if (Kp < 1 || Kp % 16 || Kp > fp6::kInt8MaxK || !sizes_ok(M, N, Kp)) return FP6_E_SHAPE;
   if (M == 0) return FP6_OK;
   if (!Xq || !sx || !Wq || !sw || !Y) return FP6_E_NULL;
   if (!aligned(Xq, 16) || !aligned(Wq, 16) || !aligned(Y, 16) || !aligned(sx, 4) || !aligned(sw, 4) ||
       !aligned(bias, 2))
     return FP6_E_ALIGN;
-  return launch_product(dtype, Product{Xq, sx, Wq, sw, bias, Y, M, N, Kp}, static_cast<hipStream_t>(stream));
+  return launch_product(dtype, Product{Xq, sx, Wq, sw, bias, Y, M, N, Kp}, variant, static_cast<hipStream_t>(stream));
+}
+
+int fp6_int8_linear(const void* Xq, const void* sx, const void* Wq, const void* sw, const void* bias, int dtype,
+                    void* Y, int64_t M, int64_t N, int64_t Kp, void* stream) {
+  return fp6_int8_linear_plan(Xq, sx, Wq, sw, bias, dtype, Y, M, N, Kp, kAuto, stream);
 }
 
 int fp6_int8_linear_tokens(int x_dtype, const void* X, int64_t ldx, const void* Wq, const void* sw,
@@ -573,7 +668,7 @@ int fp6_int8_linear_tokens(int x_dtype, const void* X, int64_t ldx, const void* 
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int st = launch_quantize(x_dtype, X, ldx, M, K, xq, sx, s);
   if (st != FP6_OK) return st;
-  return launch_product(dtype, Product{xq, sx, Wq, sw, bias, Y, M, N, kp}, s);
+  return launch_product(dtype, Product{xq, sx, Wq, sw, bias, Y, M, N, kp}, kAuto, s);
 }
 
 }  // extern "C"
