@@ -27,9 +27,14 @@ constexpr int kMaxE = static_cast<int>(fp6::kMoeMaxExperts);
 // weights' bytes, so the second pass is free.
 constexpr float kHScale = 0x1p-8f, kLoScale = 0x1p11f;
 
+constexpr int kFusedE = 128, kFusedT = 4;  // sizes up to which the choice is made inside the first product
+
 struct MoeShape {
   int T, E, k, H, I;
 };
+
+// Row groups of the second product, at most (one row block each): its counters.
+__host__ __device__ constexpr int row_groups(int64_t H) { return static_cast<int>(H / 16); }
 
 // ---------------------------------------------------------------------------
 // Router logits in 64 bits.  A product of two fp16 numbers is exact in fp32,
@@ -81,19 +86,16 @@ __device__ __forceinline__ uint64_t logit_key(double l) {
 // Top-k of one token by one wave: an expert's place is the number of experts
 // before it in the order (larger logit first, then lower index), counted
 // against every key in LDS.  Softmax in fp32 from differences formed in fp64.
-__global__ __launch_bounds__(64) void moe_topk(const double* __restrict__ logits, int E, int k, int renorm,
-                                               int* __restrict__ ids, float* __restrict__ weights) {
-  __shared__ uint64_t keys[kMaxE];
-  __shared__ int best[kMaxK];
-  __shared__ double best_l[kMaxK];
-  const int lane = threadIdx.x;
-  const int64_t t = blockIdx.x;
-  const double* l = logits + t * E;
+// keys[E], best[k], best_l[k]: the wave's own LDS; every lane < k returns its
+// place's expert and weight.
+__device__ __forceinline__ void wave_topk(const double* __restrict__ l, int E, int k, int renorm, uint64_t* keys,
+                                          int* best, double* best_l, int lane, int& id, float& weight) {
   for (int e = lane; e < E; e += 64) keys[e] = logit_key(l[e]);
-  __syncthreads();
+  __builtin_amdgcn_wave_barrier();
   for (int e = lane; e < E; e += 64) {
     const uint64_t key = keys[e];
     int place = 0;
+#pragma unroll 8
     for (int o = 0; o < E; ++o) {
       const uint64_t other = keys[o];
       place += other > key || (other == key && o < e);
@@ -103,7 +105,7 @@ __global__ __launch_bounds__(64) void moe_topk(const double* __restrict__ logits
       best_l[place] = l[e];
     }
   }
-  __syncthreads();
+  __builtin_amdgcn_wave_barrier();
   const double top = best_l[0];
   float sum = 0.0f;
   if (renorm) {
@@ -113,260 +115,429 @@ __global__ __launch_bounds__(64) void moe_topk(const double* __restrict__ logits
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
   }
+  id = -1;
+  weight = 0.0f;
   if (lane < k) {
-    ids[t * k + lane] = best[lane];
-    weights[t * k + lane] = expf(static_cast<float>(best_l[lane] - top)) / sum;
+    id = best[lane];
+    weight = expf(static_cast<float>(best_l[lane] - top)) / sum;
+  }
+}
+
+__global__ __launch_bounds__(64) void moe_topk(const double* __restrict__ logits, int E, int k, int renorm,
+                                               int* __restrict__ ids, float* __restrict__ weights) {
+  __shared__ uint64_t keys[kMaxE];
+  __shared__ int best[kMaxK];
+  __shared__ double best_l[kMaxK];
+  const int lane = threadIdx.x;
+  const int64_t t = blockIdx.x;
+  int id;
+  float w;
+  wave_topk(logits + t * E, E, k, renorm, keys, best, best_l, lane, id, w);
+  if (lane < k) {
+    ids[t * k + lane] = id;
+    weights[t * k + lane] = w;
   }
 }
 
 // ---------------------------------------------------------------------------
-// Which tokens of a group chose an expert.  A wave's lane is a token; `first`
-// is its first choice of this expert (pair index inside the group) and `w` the
-// sum of the weights of all its choices of it.
+// Both products give a workgroup of 4 waves one expert, up to 16 of its tokens
+// (the columns of the MFMAs) and (4/ks)*P row blocks of 16 rows: ks waves split
+// K, each takes P consecutive row blocks and holds a k-tile's token fragments
+// for all of them.  The weights run through a register ring of D k-tiles: as
+// soon as tile (row block p, k-tile t) is multiplied, tile (p, t+D) is
+// requested, so D*P tiles are in flight per wave; the token fragments of k-tile
+// t+1 are requested when k-tile t begins.
+//
+// Which expert: with fewer (token, choice) pairs than experts the grid has one
+// slot per pair, and the first pair of an expert takes it; else one slot per
+// expert.  Experts with more than 16 tokens have further workgroups, one per 16
+// tokens.  Workgroups without work leave at once.
+//
+// A wave's lane is a token of the group here: `first` is its first choice of
+// the expert (pair index inside the group, -1: none), `weight` the sum of the
+// weights of all its choices of it.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint64_t tokens_of(const short* ids, int tokens, int k, int e, int lane, int& first) {
-  first = -1;
-  if (lane < tokens)
-    for (int j = k - 1; j >= 0; --j)
-      if (ids[lane * k + j] == e) first = lane * k + j;
-  return __ballot(first >= 0);
-}
-
-// The group's ids as 16-bit numbers in LDS, -1 for a choice that is not served.
-__device__ __forceinline__ void load_ids(short* dst, const int* ids, int pairs, int E) {
-  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
-    const int e = ids[i];
-    dst[i] = static_cast<short>(e >= 0 && e < E ? e : -1);
+struct Choice {
+  int first;
+  float weight;
+};
+template <bool WEIGHT>
+__device__ __forceinline__ Choice choice_of(const int* __restrict__ ids, const float* __restrict__ weights, int tokens,
+                                            int k, int e, int lane) {
+  Choice c{-1, 0.0f};
+  if (lane < tokens) {
+    int id[kMaxK];
+    float w[kMaxK];
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) {  // all requested before the first is looked at
+      id[j] = -1;
+      w[j] = 0.0f;
+      if (j < k) {
+        id[j] = ids[lane * k + j];
+        if constexpr (WEIGHT) w[j] = weights[lane * k + j];
+      }
+    }
+#pragma unroll
+    for (int j = kMaxK - 1; j >= 0; --j)
+      if (j < k && id[j] == e) c.first = lane * k + j;
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+      if (j < k && id[j] == e) c.weight += w[j];
   }
+  return c;
 }
 
-// ---------------------------------------------------------------------------
-// Gate and up products with the gated activation.  A workgroup takes one
-// expert and 8/ks row blocks (16 rows of the gate and the same 16 of the up
-// projection each); ks waves split K = H of a row block and add through LDS.
-// The columns of the MFMAs are the expert's tokens, gathered; columns behind
-// the last repeat the first and are not stored.
-// ---------------------------------------------------------------------------
-template <int F, int MT>
-__global__ __launch_bounds__(512) void moe_gate_up(const _Float16* __restrict__ X, const int* __restrict__ ids_g,
-                                                   const float* __restrict__ weights_g,
+// Whether this workgroup has work: mask of the expert's tokens, its chunk of 16
+// of them, and (slots by pair) whether the slot's pair is the expert's first.
+__device__ __forceinline__ bool has_work(uint64_t mask, int first, int chunk, int by_pair, int slot) {
+  if (16 * chunk >= __popcll(mask)) return false;
+  if (!by_pair) return true;
+  return __builtin_amdgcn_readlane(first, __ffsll(static_cast<unsigned long long>(mask)) - 1) == slot;
+}
+
+// Gate and up products with the gated activation; row block p of the gate and
+// of the up projection go together.  FUSED (few tokens, few experts): the
+// choice is made here from the logits, wave t for token t, by every workgroup
+// for itself, and written out by the first one.  The first workgroup also clears
+// the counters of the second product.
+template <int F, int P, int D, bool FUSED>
+__global__ __launch_bounds__(256) void moe_gate_up(const _Float16* __restrict__ X, const double* __restrict__ logits,
+                                                   int* __restrict__ ids_g, float* __restrict__ weights_g,
                                                    const u32x4* __restrict__ wp, const _Float16* __restrict__ scales,
-                                                   _Float16* __restrict__ hi, _Float16* __restrict__ lo, MoeShape s,
-                                                   int ks, int by_pair) {
-  __shared__ short ids[kGroup * kMaxK];
-  __shared__ short col_token[kGroup], col_pair[kGroup];
-  __shared__ float col_w[kGroup];
-  __shared__ float4v red[8][2 * MT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+                                                   _Float16* __restrict__ hi, _Float16* __restrict__ lo,
+                                                   unsigned* __restrict__ counters, MoeShape s, int ks, int by_pair,
+                                                   int slots, int renorm) {
+  __shared__ short col_token[4][kGroup], col_pair[4][kGroup];
+  __shared__ float col_w[4][kGroup];
+  __shared__ float4v red[4][2 * P][64];
+  __shared__ uint64_t keys[FUSED ? 4 : 1][FUSED ? kFusedE : 1];
+  __shared__ int best[FUSED ? 4 : 1][kMaxK];
+  __shared__ double best_l[FUSED ? 4 : 1][kMaxK];
+  __shared__ int f_ids[FUSED ? 4 * kMaxK : 1];
+  __shared__ float f_w[FUSED ? 4 * kMaxK : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int t0 = blockIdx.z * kGroup;
   const int tokens = s.T - t0 < kGroup ? s.T - t0 : kGroup;
-  const int pairs = tokens * s.k;
-  load_ids(ids, ids_g + static_cast<int64_t>(t0) * s.k, pairs, s.E);
-  __syncthreads();
-  // Fewer pairs than experts: the grid has one slot per pair, and the first
-  // pair of an expert takes it; else one slot per expert.
-  int e = blockIdx.y;
+  const bool first_wg = blockIdx.x == 0 && blockIdx.y == 0;
+  if (first_wg && blockIdx.z == 0)
+    for (int i = threadIdx.x; i < row_groups(s.H); i += 256) counters[i] = 0u;
+  const int* ids = ids_g + static_cast<int64_t>(t0) * s.k;
+  const float* weights = weights_g + static_cast<int64_t>(t0) * s.k;
+  if constexpr (FUSED) {
+    if (wave < tokens) {
+      int id;
+      float w;
+      wave_topk(logits + wave * s.E, s.E, s.k, renorm, keys[wave], best[wave], best_l[wave], lane, id, w);
+      if (lane < s.k) {
+        f_ids[wave * s.k + lane] = id;
+        f_w[wave * s.k + lane] = w;
+        if (first_wg) {
+          ids_g[wave * s.k + lane] = id;
+          weights_g[wave * s.k + lane] = w;
+        }
+      }
+    }
+    __syncthreads();
+    ids = f_ids;
+    weights = f_w;
+  }
+  const int chunk = blockIdx.y / slots, slot = blockIdx.y - chunk * slots;
+  int e = slot;
   if (by_pair) {
-    if (e >= pairs) return;
-    const int p = e;
-    e = ids[p];
-    if (e < 0) return;
-    for (int q = 0; q < p; ++q)
-      if (ids[q] == e) return;
+    if (slot >= tokens * s.k) return;
+    e = __builtin_amdgcn_readfirstlane(ids[slot]);
+    if (e < 0 || e >= s.E) return;
   }
-  int first;
-  const uint64_t mask = tokens_of(ids, tokens, s.k, e, lane, first);
-  const int n = __popcll(mask);
-  if (n == 0) return;
-  if (wave == 0 && first >= 0) {
-    const int c = __popcll(mask & ((uint64_t(1) << lane) - 1));
-    float w = 0.0f;
-    for (int j = 0; j < s.k; ++j)
-      if (ids[lane * s.k + j] == e) w += weights_g[static_cast<int64_t>(t0 + lane) * s.k + j];
-    col_token[c] = static_cast<short>(lane);
-    col_pair[c] = static_cast<short>(first);
-    col_w[c] = w;
-  }
-  __syncthreads();
+  const Choice ch = choice_of<true>(ids, weights, tokens, s.k, e, lane);
 
   const int rb = wave / ks, kslice = wave - rb * ks;
   const int iblocks = s.I >> 4, ktiles = s.H >> 8;
-  int nb = blockIdx.x * (8 / ks) + rb;
-  const bool live = nb < iblocks;
-  if (!live) nb = iblocks - 1;
-  const int64_t nblocks = 2 * static_cast<int64_t>(iblocks);
-  const int64_t kstr = nblocks * Fmt<F>::kTileQuads;
+  const int nb = (blockIdx.x * (4 / ks) + rb) * P;
+  const int64_t kstr = 2 * static_cast<int64_t>(iblocks) * Fmt<F>::kTileQuads;
   const u32x4* wg = wp + static_cast<int64_t>(e) * ktiles * kstr + nb * static_cast<int64_t>(Fmt<F>::kTileQuads) + lane;
   const u32x4* wu = wg + static_cast<int64_t>(iblocks) * Fmt<F>::kTileQuads;
+  const int kt0 = kslice * ktiles / ks, kt1 = (kslice + 1) * ktiles / ks;  // never empty: ks <= ktiles
+  typename Fmt<F>::Tile tg[D][P], tu[D][P];
+  _Float16 sg[P], su[P];
   const _Float16* sc = scales + static_cast<int64_t>(e) * 2 * s.I + nb * 16 + r;
-  const half2v sg = scale2_of<F>(sc[0]), su = scale2_of<F>(sc[s.I]);
-  const int kt0 = kslice * ktiles / ks, kt1 = (kslice + 1) * ktiles / ks;
-
-  for (int c0 = 0; c0 < n; c0 += 16 * MT) {
-    const _Float16* xr[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int c = c0 + 16 * m + r;
-      xr[m] = X + static_cast<int64_t>(t0 + col_token[c < n ? c : 0]) * s.H + 8 * g;
+  for (int d = 0; d < D; ++d) {
+    const int64_t at = (kt0 + d < kt1 ? kt0 + d : kt0) * kstr;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      Fmt<F>::template load<true>(tg[d][p], wg + at + p * Fmt<F>::kTileQuads, lane);
+      Fmt<F>::template load<true>(tu[d][p], wu + at + p * Fmt<F>::kTileQuads, lane);
     }
-    float4v ag[MT], au[MT];
+  }
 #pragma unroll
-    for (int m = 0; m < MT; ++m) ag[m] = au[m] = float4v{0.f, 0.f, 0.f, 0.f};
-    for (int kt = kt0; kt < kt1; ++kt) {
-      typename Fmt<F>::Tile tg, tu;
-      Fmt<F>::template load<true>(tg, wg + kt * kstr, lane);
-      Fmt<F>::template load<true>(tu, wu + kt * kstr, lane);
-      half8v xf[MT][8];
+  for (int p = 0; p < P; ++p) {
+    sg[p] = sc[16 * p];
+    su[p] = sc[s.I + 16 * p];
+  }
+  const uint64_t mask = __ballot(ch.first >= 0);
+  if (!has_work(mask, ch.first, chunk, by_pair, slot)) return;
+  const int n = __popcll(mask);
+  if (ch.first >= 0) {
+    const int c = __popcll(mask & ((uint64_t(1) << lane) - 1));
+    col_token[wave][c] = static_cast<short>(lane);
+    col_pair[wave][c] = static_cast<short>(ch.first);
+    col_w[wave][c] = ch.weight;
+  }
+  __builtin_amdgcn_wave_barrier();
+  // Column r; columns behind the expert's last token repeat the chunk's first and are not stored.
+  const int c = 16 * chunk + r < n ? 16 * chunk + r : 16 * chunk;
+  const _Float16* xr = X + static_cast<int64_t>(t0 + col_token[wave][c]) * s.H + 8 * g;
+  half8v xf[2][8];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+  for (int j = 0; j < 8; ++j) xf[0][j] = *reinterpret_cast<const half8v*>(xr + kt0 * 256 + 32 * j);
+  float4v ag[P], au[P];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) xf[m][j] = *reinterpret_cast<const half8v*>(xr[m] + kt * 256 + 32 * j);
+  for (int p = 0; p < P; ++p) ag[p] = au[p] = float4v{0.f, 0.f, 0.f, 0.f};
+
+  auto tile = [&](int kt, auto CUR) {
+    constexpr int cur = decltype(CUR)::value;
+    const int next = kt + 1 < kt1 ? kt + 1 : kt;  // behind the end: a stand-in
+#pragma unroll
+    for (int j = 0; j < 8; ++j) xf[1 - cur][j] = *reinterpret_cast<const half8v*>(xr + next * 256 + 32 * j);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const half2v s2g = scale2_of<F>(sg[p]), s2u = scale2_of<F>(su[p]);
       auto step = [&](auto J) {
         constexpr int j = decltype(J)::value;
-        const half8v a = Fmt<F>::template step<j>(tg, sg), b = Fmt<F>::template step<j>(tu, su);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          ag[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, xf[m][j], ag[m], 0, 0, 0);
-          au[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, xf[m][j], au[m], 0, 0, 0);
-        }
+        ag[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(Fmt<F>::template step<j>(tg[cur % D][p], s2g), xf[cur][j], ag[p], 0, 0, 0);
+        au[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(Fmt<F>::template step<j>(tu[cur % D][p], s2u), xf[cur][j], au[p], 0, 0, 0);
       };
       step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
       step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
       step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
       step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      red[wave][2 * m][lane] = ag[m];
-      red[wave][2 * m + 1][lane] = au[m];
-    }
-    __syncthreads();
-    // Wave (rb, kslice) sums and stores the column blocks kslice, kslice + ks, ...
-    for (int m = kslice; m < MT; m += ks) {
-      const int c = c0 + 16 * m + r;
-      if (live && c < n) {
-        float4v vg = red[rb * ks][2 * m][lane], vu = red[rb * ks][2 * m + 1][lane];
-        for (int w = 1; w < ks; ++w) {
-          vg += red[rb * ks + w][2 * m][lane];
-          vu += red[rb * ks + w][2 * m + 1][lane];
-        }
-        half4v oh, ol;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float h = (vg[i] / (1.0f + expf(-vg[i]))) * vu[i] * col_w[c] * kHScale;
-          oh[i] = static_cast<_Float16>(h);
-          const float hf = static_cast<float>(oh[i]);
-          ol[i] = __builtin_isinf(hf) ? static_cast<_Float16>(0.0f) : static_cast<_Float16>((h - hf) * kLoScale);
-        }
-        const int64_t at = (static_cast<int64_t>(t0) * s.k + col_pair[c]) * s.I + nb * 16 + 4 * g;
-        *reinterpret_cast<half4v*>(hi + at) = oh;
-        *reinterpret_cast<half4v*>(lo + at) = ol;
+      __builtin_amdgcn_sched_barrier(0);
+      if (kt + D < kt1) {
+        Fmt<F>::template load<true>(tg[cur % D][p], wg + (kt + D) * kstr + p * Fmt<F>::kTileQuads, lane);
+        Fmt<F>::template load<true>(tu[cur % D][p], wu + (kt + D) * kstr + p * Fmt<F>::kTileQuads, lane);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __syncthreads();
+  };
+  int kt = kt0;
+  for (; kt + 2 <= kt1; kt += 2) {
+    tile(kt, std::integral_constant<int, 0>{});
+    tile(kt + 1, std::integral_constant<int, 1>{});
+  }
+  if (kt < kt1) tile(kt, std::integral_constant<int, 0>{});
+
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    red[wave][2 * p][lane] = ag[p];
+    red[wave][2 * p + 1][lane] = au[p];
+  }
+  __syncthreads();
+  // Wave (rb, kslice) sums and stores the row blocks kslice, kslice + ks, ...
+  if (16 * chunk + r < n) {
+    const int64_t at = (static_cast<int64_t>(t0) * s.k + col_pair[wave][c]) * s.I + nb * 16 + 4 * g;
+    const float w = col_w[wave][c];
+    for (int p = kslice; p < P; p += ks) {
+      float4v vg = red[rb * ks][2 * p][lane], vu = red[rb * ks][2 * p + 1][lane];
+      for (int q = 1; q < ks; ++q) {
+        vg += red[rb * ks + q][2 * p][lane];
+        vu += red[rb * ks + q][2 * p + 1][lane];
+      }
+      half4v oh, ol;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float h = (vg[i] / (1.0f + expf(-vg[i]))) * vu[i] * w * kHScale;
+        oh[i] = static_cast<_Float16>(h);
+        const float hf = static_cast<float>(oh[i]);
+        ol[i] = __builtin_isinf(hf) ? static_cast<_Float16>(0.0f) : static_cast<_Float16>((h - hf) * kLoScale);
+      }
+      *reinterpret_cast<half4v*>(hi + at + 16 * p) = oh;
+      *reinterpret_cast<half4v*>(lo + at + 16 * p) = ol;
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Down product and the sum over experts.  A workgroup owns 16 rows of the
-// output for all tokens of the group; its waves share the list of (expert,
-// k-tile) of the experts that any token chose, in equal contiguous parts.  The
-// weights of the choice are already in h, so a wave simply adds: the MFMA
-// columns are an expert's tokens, gathered, and after its last tile of an
-// expert the wave adds them to its own [token][row] sums in LDS.  The waves'
-// sums are added in wave order and rounded once.
+// Down product and the sum over experts.  Every workgroup stores its expert's
+// part of the outputs, one fp32 row per pair (the weight of the choice is
+// already in h); each output adds its token's parts in the order of the choices
+// and is rounded once.  With few tokens (SUM) this happens in the same kernel:
+// parts are stored device-wide, a workgroup counts itself at its row group, and
+// the last one there (none waits for another) adds.  With more, that last
+// workgroup would add for many tokens alone (64 tokens, 64 experts, 2048x1024:
+// 181 us against 52 with a kernel of its own).
 // ---------------------------------------------------------------------------
-template <int F, int NW, int TT>
-__global__ __launch_bounds__(64 * NW) void moe_down(const _Float16* __restrict__ hi, const _Float16* __restrict__ lo,
-                                                    const int* __restrict__ ids_g, const u32x4* __restrict__ wp,
-                                                    const _Float16* __restrict__ scales, _Float16* __restrict__ Y,
-                                                    MoeShape s) {
-  __shared__ short ids[kGroup * kMaxK];
-  __shared__ short active[kMaxE];
-  __shared__ uint64_t chosen[kMaxE / 64];
-  __shared__ short cols[NW][kGroup], pair_of[NW][kGroup];
-  __shared__ float ysum[NW][TT][16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+template <typename LOAD>
+__device__ __forceinline__ void sum_choices(const int* __restrict__ ids, const MoeShape& s, LOAD load, _Float16* y) {
+  float4v v[kMaxK];
+  int id[kMaxK];
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) id[j] = j < s.k ? ids[j] : -1;
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    bool use = id[j] >= 0 && id[j] < s.E;
+#pragma unroll
+    for (int o = 0; o < j; ++o) use = use && id[o] != id[j];  // the same expert again: counted with the first
+    v[j] = float4v{0.f, 0.f, 0.f, 0.f};
+    if (use) v[j] = load(j);
+  }
+  float4v sum = v[0];
+#pragma unroll
+  for (int j = 1; j < kMaxK; ++j)
+    if (j < s.k) sum += v[j];
+  half4v o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = static_cast<_Float16>(sum[i] * (1.0f / kHScale));
+  *reinterpret_cast<half4v*>(y) = o;
+}
+
+template <int F, int P, int D, bool SUM>
+__global__ __launch_bounds__(256) void moe_down(const _Float16* __restrict__ hi, const _Float16* __restrict__ lo,
+                                                const int* __restrict__ ids_g, const u32x4* __restrict__ wp,
+                                                const _Float16* __restrict__ scales, float* __restrict__ part,
+                                                unsigned* __restrict__ counters, _Float16* __restrict__ Y, MoeShape s,
+                                                int ks, int by_pair, int slots) {
+  __shared__ short col_pair[4][kGroup];
+  __shared__ float4v red[4][P][64];
+  __shared__ unsigned arrived;
+  constexpr int kSc1 = 16;                // cache policy: device scope
+  constexpr int kRsrcWord3 = 0x00020000;  // raw 32-bit buffer, gfx9 family
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int t0 = blockIdx.z * kGroup;
   const int tokens = s.T - t0 < kGroup ? s.T - t0 : kGroup;
-  const int pairs = tokens * s.k;
-  load_ids(ids, ids_g + static_cast<int64_t>(t0) * s.k, pairs, s.E);
-  if (threadIdx.x < kMaxE / 64) chosen[threadIdx.x] = 0;
-  for (int i = threadIdx.x; i < NW * TT * 16; i += 64 * NW) (&ysum[0][0][0])[i] = 0.0f;
-  __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += 64 * NW) {
-    const int e = ids[i];
-    if (e >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&chosen[e >> 6]), 1ull << (e & 63));
-  }
-  __syncthreads();
-  int na = 0;
-  for (int b = 0; 64 * b < s.E; ++b) {
-    const uint64_t m = chosen[b];
-    if (wave == 0 && ((m >> lane) & 1)) active[na + __popcll(m & ((uint64_t(1) << lane) - 1))] = static_cast<short>(64 * b + lane);
-    na += __popcll(m);
-  }
-  __syncthreads();
+  const int* ids = ids_g + static_cast<int64_t>(t0) * s.k;
+  const int chunk = blockIdx.y / slots, slot = blockIdx.y - chunk * slots;
+  const int rows0 = blockIdx.x * (4 / ks) * P * 16;  // this workgroup's rows of the output
+  float* parts = part + static_cast<int64_t>(t0) * s.k * s.H;
+  [[maybe_unused]] __amdgpu_buffer_rsrc_t rsrc;  // SUM: at most 4 tokens' parts, below 2^31 bytes
+  if constexpr (SUM)
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(parts, static_cast<short>(0), tokens * s.k * s.H * 4, kRsrcWord3);
 
-  const int nb = blockIdx.x, ktiles = s.I >> 8;
-  const int64_t nblocks = s.H >> 4, kstr = nblocks * Fmt<F>::kTileQuads;
-  const int total = na * ktiles;
-  const int f0 = static_cast<int>(static_cast<int64_t>(wave) * total / NW);
-  const int f1 = static_cast<int>(static_cast<int64_t>(wave + 1) * total / NW);
-  for (int f = f0; f < f1;) {
-    const int a = f / ktiles, kt0 = f - a * ktiles, e = active[a];
-    const int kt1 = f1 - f < ktiles - kt0 ? kt0 + (f1 - f) : ktiles;
-    f += kt1 - kt0;
-    int first;
-    const uint64_t mask = tokens_of(ids, tokens, s.k, e, lane, first);
-    const int n = __popcll(mask);
-    if (first >= 0) {
-      const int c = __popcll(mask & ((uint64_t(1) << lane) - 1));
-      cols[wave][c] = static_cast<short>(lane);
-      pair_of[wave][c] = static_cast<short>(first);
+  int e = slot;
+  bool work = true;
+  if (by_pair) {
+    work = slot < tokens * s.k;
+    if (work) {
+      e = __builtin_amdgcn_readfirstlane(ids[slot]);
+      work = e >= 0 && e < s.E;
     }
-    __builtin_amdgcn_wave_barrier();
-    const half2v s2 = scale2_of<F>(scales[static_cast<int64_t>(e) * s.H + nb * 16 + r]);
+  }
+  if (work) {
+    const Choice ch = choice_of<false>(ids, nullptr, tokens, s.k, e, lane);
+    const int rb = wave / ks, kslice = wave - rb * ks;
+    const int ktiles = s.I >> 8;
+    const int nb = (blockIdx.x * (4 / ks) + rb) * P;
+    const int64_t kstr = static_cast<int64_t>(s.H >> 4) * Fmt<F>::kTileQuads;
     const u32x4* w = wp + static_cast<int64_t>(e) * ktiles * kstr + nb * static_cast<int64_t>(Fmt<F>::kTileQuads) + lane;
-    for (int c0 = 0; c0 < n; c0 += 16) {
-      const int c = c0 + r;
-      const int64_t at = (static_cast<int64_t>(t0) * s.k + pair_of[wave][c < n ? c : 0]) * s.I + 8 * g;
-      float4v ah = {0.f, 0.f, 0.f, 0.f}, al = {0.f, 0.f, 0.f, 0.f};
-      for (int kt = kt0; kt < kt1; ++kt) {
-        typename Fmt<F>::Tile t;
-        Fmt<F>::template load<true>(t, w + kt * kstr, lane);
-        half8v fh[8], fl[8];
+    const int kt0 = kslice * ktiles / ks, kt1 = (kslice + 1) * ktiles / ks;
+    typename Fmt<F>::Tile tw[D][P];
+    _Float16 sw[P];
+    const _Float16* sc = scales + static_cast<int64_t>(e) * s.H + nb * 16 + r;
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        Fmt<F>::template load<true>(tw[d][p], w + (kt0 + d < kt1 ? kt0 + d : kt0) * kstr + p * Fmt<F>::kTileQuads, lane);
+#pragma unroll
+    for (int p = 0; p < P; ++p) sw[p] = sc[16 * p];
+    const uint64_t mask = __ballot(ch.first >= 0);
+    work = has_work(mask, ch.first, chunk, by_pair, slot);
+    if (work) {
+      const int n = __popcll(mask);
+      if (ch.first >= 0) col_pair[wave][__popcll(mask & ((uint64_t(1) << lane) - 1))] = static_cast<short>(ch.first);
+      __builtin_amdgcn_wave_barrier();
+      const int c = 16 * chunk + r < n ? 16 * chunk + r : 16 * chunk;
+      const int pair = col_pair[wave][c];
+      const int64_t at = (static_cast<int64_t>(t0) * s.k + pair) * s.I + 8 * g;
+      const _Float16 *hr = hi + at, *lr = lo + at;
+      half8v fh[2][8], fl[2][8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        fh[0][j] = *reinterpret_cast<const half8v*>(hr + kt0 * 256 + 32 * j);
+        fl[0][j] = *reinterpret_cast<const half8v*>(lr + kt0 * 256 + 32 * j);
+      }
+      float4v ah[P], al[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) ah[p] = al[p] = float4v{0.f, 0.f, 0.f, 0.f};
+      auto tile = [&](int kt, auto CUR) {
+        constexpr int cur = decltype(CUR)::value;
+        const int next = kt + 1 < kt1 ? kt + 1 : kt;  // behind the end: a stand-in
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          fh[j] = *reinterpret_cast<const half8v*>(hi + at + kt * 256 + 32 * j);
-          fl[j] = *reinterpret_cast<const half8v*>(lo + at + kt * 256 + 32 * j);
+          fh[1 - cur][j] = *reinterpret_cast<const half8v*>(hr + next * 256 + 32 * j);
+          fl[1 - cur][j] = *reinterpret_cast<const half8v*>(lr + next * 256 + 32 * j);
         }
-        auto step = [&](auto J) {
-          constexpr int j = decltype(J)::value;
-          const half8v av = Fmt<F>::template step<j>(t, s2);
-          ah = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, fh[j], ah, 0, 0, 0);
-          al = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, fl[j], al, 0, 0, 0);
-        };
-        step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
-        step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
-        step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
-        step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const half2v s2 = scale2_of<F>(sw[p]);
+          auto step = [&](auto J) {
+            constexpr int j = decltype(J)::value;
+            const half8v a = Fmt<F>::template step<j>(tw[cur % D][p], s2);
+            ah[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fh[cur][j], ah[p], 0, 0, 0);
+            al[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fl[cur][j], al[p], 0, 0, 0);
+          };
+          step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
+          step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
+          step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
+          step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
+          __builtin_amdgcn_sched_barrier(0);
+          if (kt + D < kt1)
+            Fmt<F>::template load<true>(tw[cur % D][p], w + (kt + D) * kstr + p * Fmt<F>::kTileQuads, lane);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      int kt = kt0;
+      for (; kt + 2 <= kt1; kt += 2) {
+        tile(kt, std::integral_constant<int, 0>{});
+        tile(kt + 1, std::integral_constant<int, 1>{});
       }
-      if (c < n) {
-        float4v* y = reinterpret_cast<float4v*>(&ysum[wave][cols[wave][c]][4 * g]);
-        *y = *y + (ah + al * (1.0f / kLoScale));
+      if (kt < kt1) tile(kt, std::integral_constant<int, 0>{});
+#pragma unroll
+      for (int p = 0; p < P; ++p) red[wave][p][lane] = ah[p] + al[p] * (1.0f / kLoScale);
+      __syncthreads();
+      if (16 * chunk + r < n) {
+        const int64_t dst = static_cast<int64_t>(pair) * s.H + rows0 + rb * P * 16 + 4 * g;
+        for (int p = kslice; p < P; p += ks) {
+          float4v v = red[rb * ks][p][lane];
+          for (int q = 1; q < ks; ++q) v += red[rb * ks + q][p][lane];
+          if constexpr (SUM)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, static_cast<int>(dst + 16 * p) * 4, 0, kSc1);
+          else
+            *reinterpret_cast<float4v*>(parts + dst + 16 * p) = v;
+        }
       }
     }
-    __builtin_amdgcn_wave_barrier();
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < tokens * 16; i += 64 * NW) {
-    const int t = i >> 4, row = i & 15;
-    float y = ysum[0][t][row];
-    for (int w = 1; w < NW; ++w) y += ysum[w][t][row];
-    Y[static_cast<int64_t>(t0 + t) * s.H + nb * 16 + row] = static_cast<_Float16>(y * (1.0f / kHScale));
+  if constexpr (SUM) {
+    __builtin_amdgcn_s_waitcnt(0);  // this wave's parts are stored
+    __syncthreads();
+    if (threadIdx.x == 0)
+      arrived = __hip_atomic_fetch_add(counters + blockIdx.x, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (arrived != gridDim.y - 1) return;
+    const int quads = (4 / ks) * P * 4;  // 16-byte units of the row group
+    for (int i = threadIdx.x; i < tokens * quads; i += 256) {
+      const int t = i / quads, row = rows0 + 4 * (i - t * quads);
+      sum_choices(ids + t * s.k, s, [&](int j) {
+        return __builtin_bit_cast(float4v, __builtin_amdgcn_raw_buffer_load_b128(
+                                               rsrc, ((t * s.k + j) * s.H + row) * 4, 0, kSc1));
+      }, Y + static_cast<int64_t>(t) * s.H + row);
+    }
   }
+}
+
+// Many tokens: the sum in a kernel of its own, 4 rows of a token per thread.
+__global__ __launch_bounds__(256) void moe_sum(const float* __restrict__ part, const int* __restrict__ ids,
+                                               _Float16* __restrict__ Y, MoeShape s) {
+  const int64_t t = blockIdx.y;
+  const int row = 4 * (blockIdx.x * 256 + threadIdx.x);
+  if (row >= s.H) return;
+  const float* p = part + t * s.k * s.H + row;
+  sum_choices(ids + t * s.k, s, [&](int j) { return *reinterpret_cast<const float4v*>(p + static_cast<int64_t>(j) * s.H); },
+              Y + t * s.H + row);
 }
 
 // ---------------------------------------------------------------------------
@@ -384,24 +555,29 @@ bool moe_sizes_ok(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Workspace {
-  size_t logits, hi, lo, bytes;
+  size_t logits, hi, lo, part, counters, bytes;
 };
-Workspace workspace_of(int64_t T, int64_t E, int64_t k, int64_t I) {
+Workspace workspace_of(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
   Workspace w;
+  const size_t pairs = static_cast<size_t>(T) * k;
   w.logits = 0;
   w.hi = round256(static_cast<size_t>(T) * E * sizeof(double));
-  w.lo = w.hi + round256(static_cast<size_t>(T) * k * I * 2);
-  w.bytes = w.lo + round256(static_cast<size_t>(T) * k * I * 2);
+  w.lo = w.hi + round256(pairs * I * 2);
+  w.part = w.lo + round256(pairs * I * 2);
+  w.counters = w.part + round256(pairs * H * sizeof(float));
+  w.bytes = w.counters + row_groups(H) * sizeof(unsigned);
   return w;
 }
 
 struct MoeCall {
   const _Float16* X;
-  const int* ids;
-  const float* weights;
+  int* ids;        // written only where the layer makes the choice
+  float* weights;
   const u32x4 *gate_up, *down;
   const _Float16 *gate_up_scales, *down_scales;
   _Float16 *Y, *hi, *lo;
+  float* part;
+  unsigned* counters;
   MoeShape s;
   hipStream_t stream;
 };
@@ -410,44 +586,108 @@ int moe_launch(const void* kern, dim3 grid, dim3 block, void** args, hipStream_t
   return hipLaunchKernel(kern, grid, block, args, 0, stream) == hipSuccess ? FP6_OK : FP6_E_HIP;
 }
 
+// Waves that split K and row blocks per wave: the most work per workgroup
+// (fewer prologues, token fragments used for more rows) that still gives every
+// CU two workgroups, counting every slot as used.
+struct Split {
+  int ks, p;
+};
+Split choose_split(int64_t row_blocks, int64_t ktiles, int64_t slots, int cus) {
+  Split s{4, 1};
+  for (const Split c : {Split{1, 4}, Split{2, 4}, Split{4, 4}, Split{4, 2}}) {
+    if (c.ks <= ktiles && slots * (row_blocks / (4 / c.ks * c.p)) >= 2 * cus) {
+      s = c;
+      break;
+    }
+  }
+  while (s.ks > ktiles) s.ks >>= 1;
+  return s;
+}
+
+int device_cus() {
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+    cus = 256;
+  return cus;
+}
+
+// logits: of fpx_moe_layer, whose choice is not made yet (then the first
+// product makes it); null: ids and weights are there.
 template <int F>
-int launch_experts(const MoeCall& c) {
+int launch_experts(const MoeCall& c, const double* logits, int renorm) {
   MoeShape s = c.s;
   const int group_tokens = s.T < kGroup ? s.T : kGroup;
   const unsigned groups = static_cast<unsigned>(fpx_ceil_div(s.T, kGroup));
-  int ks = 8;
-  while (ks > 1 && ks > s.H / 256) ks >>= 1;
   int by_pair = group_tokens * s.k < s.E;
-  const unsigned slots = by_pair ? group_tokens * s.k : s.E;
+  int slots = by_pair ? group_tokens * s.k : s.E;
+  const unsigned grid_y = static_cast<unsigned>(slots) * static_cast<unsigned>(fpx_ceil_div(group_tokens, 16));
+  const int cus = device_cus();
   const _Float16* X = c.X;
-  const int* ids = c.ids;
-  const float* weights = c.weights;
+  int* ids = c.ids;
+  float* weights = c.weights;
   const u32x4* w = c.gate_up;
   const _Float16* sc = c.gate_up_scales;
   _Float16 *hi = c.hi, *lo = c.lo, *Y = c.Y;
+  unsigned* counters = c.counters;
+  float* part = c.part;
   {
-    void* args[] = {&X, &ids, &weights, &w, &sc, &hi, &lo, &s, &ks, &by_pair};
-    const dim3 grid(static_cast<unsigned>(fpx_ceil_div(s.I / 16, 8 / ks)), slots, groups);
-    const void* kern = group_tokens <= 16 ? reinterpret_cast<const void*>(&moe_gate_up<F, 1>)
-                                          : reinterpret_cast<const void*>(&moe_gate_up<F, 2>);
-    const int st = moe_launch(kern, grid, dim3(512), args, c.stream);
+    Split sp = choose_split(s.I / 16, s.H / 256, slots, cus);
+    void* args[] = {&X, &logits, &ids, &weights, &w, &sc, &hi, &lo, &counters, &s, &sp.ks, &by_pair, &slots, &renorm};
+    const dim3 grid(static_cast<unsigned>(s.I / 16 / (4 / sp.ks * sp.p)), grid_y, groups);
+    const void* kern = nullptr;
+    if (logits)
+      kern = sp.p == 4   ? reinterpret_cast<const void*>(&moe_gate_up<F, 4, 1, true>)
+             : sp.p == 2 ? reinterpret_cast<const void*>(&moe_gate_up<F, 2, 1, true>)
+                         : reinterpret_cast<const void*>(&moe_gate_up<F, 1, 2, true>);
+    else
+      kern = sp.p == 4   ? reinterpret_cast<const void*>(&moe_gate_up<F, 4, 1, false>)
+             : sp.p == 2 ? reinterpret_cast<const void*>(&moe_gate_up<F, 2, 1, false>)
+                         : reinterpret_cast<const void*>(&moe_gate_up<F, 1, 2, false>);
+    const int st = moe_launch(kern, grid, dim3(256), args, c.stream);
     if (st != FP6_OK) return st;
   }
   w = c.down;
   sc = c.down_scales;
-  void* args[] = {&hi, &lo, &ids, &w, &sc, &Y, &s};
-  const dim3 grid(static_cast<unsigned>(s.H / 16), 1, groups);
-  const void* kern = group_tokens <= 16 ? reinterpret_cast<const void*>(&moe_down<F, 16, 16>)
-                                        : reinterpret_cast<const void*>(&moe_down<F, 8, 64>);
-  return moe_launch(kern, grid, dim3(group_tokens <= 16 ? 1024 : 512), args, c.stream);
+  Split sp = choose_split(s.H / 16, s.I / 256, slots, cus);
+  void* args[] = {&hi, &lo, &ids, &w, &sc, &part, &counters, &Y, &s, &sp.ks, &by_pair, &slots};
+  const dim3 grid(static_cast<unsigned>(s.H / 16 / (4 / sp.ks * sp.p)), grid_y, groups);
+  const bool sum = s.T <= kFusedT;
+  const void* kern = nullptr;
+  if (sum)
+    kern = sp.p == 4   ? reinterpret_cast<const void*>(&moe_down<F, 4, 1, true>)
+           : sp.p == 2 ? reinterpret_cast<const void*>(&moe_down<F, 2, 1, true>)
+                       : reinterpret_cast<const void*>(&moe_down<F, 1, 2, true>);
+  else
+    kern = sp.p == 4   ? reinterpret_cast<const void*>(&moe_down<F, 4, 1, false>)
+           : sp.p == 2 ? reinterpret_cast<const void*>(&moe_down<F, 2, 1, false>)
+                       : reinterpret_cast<const void*>(&moe_down<F, 1, 2, false>);
+  const int st = moe_launch(kern, grid, dim3(256), args, c.stream);
+  if (st != FP6_OK || sum) return st;
+  void* sum_args[] = {&part, &ids, &Y, &s};
+  // The grid's second dimension takes T <= 65536 tokens in two parts.
+  for (int t = 0; t < s.T; t += 32768) {
+    const float* pt = part + static_cast<int64_t>(t) * s.k * s.H;
+    const int* it = ids + static_cast<int64_t>(t) * s.k;
+    _Float16* yt = Y + static_cast<int64_t>(t) * s.H;
+    sum_args[0] = &pt;
+    sum_args[1] = &it;
+    sum_args[2] = &yt;
+    const int rest = s.T - t < 32768 ? s.T - t : 32768;
+    const int r = moe_launch(reinterpret_cast<const void*>(&moe_sum),
+                             dim3(static_cast<unsigned>(fpx_ceil_div(s.H, 1024)), static_cast<unsigned>(rest)), dim3(256),
+                             sum_args, c.stream);
+    if (r != FP6_OK) return r;
+  }
+  return FP6_OK;
 }
 
-int launch_experts_format(int format, const MoeCall& c) {
+int launch_experts_format(int format, const MoeCall& c, const double* logits = nullptr, int renorm = 0) {
   switch (format) {
-    case FPX_E3M2: return launch_experts<kE3M2>(c);
-    case FPX_E2M3: return launch_experts<kE2M3>(c);
-    case FPX_E2M2: return launch_experts<kE2M2>(c);
-    case FPX_E2M1: return launch_experts<kE2M1>(c);
+    case FPX_E3M2: return launch_experts<kE3M2>(c, logits, renorm);
+    case FPX_E2M3: return launch_experts<kE2M3>(c, logits, renorm);
+    case FPX_E2M2: return launch_experts<kE2M2>(c, logits, renorm);
+    case FPX_E2M1: return launch_experts<kE2M1>(c, logits, renorm);
     default: return FP6_E_VALUE;
   }
 }
@@ -478,12 +718,12 @@ int check_experts(int format, const void* X, const void* ids, const void* weight
 MoeCall make_call(const void* X, const void* ids, const void* weights, const void* gate_up,
                   const void* gate_up_scales, const void* down, const void* down_scales, void* Y, int64_t T, int64_t E,
                   int64_t k, int64_t H, int64_t I, void* workspace, void* stream) {
-  const Workspace w = workspace_of(T, E, k, I);
+  const Workspace w = workspace_of(T, E, k, H, I);
   char* ws = static_cast<char*>(workspace);
   MoeCall c;
   c.X = static_cast<const _Float16*>(X);
-  c.ids = static_cast<const int*>(ids);
-  c.weights = static_cast<const float*>(weights);
+  c.ids = const_cast<int*>(static_cast<const int*>(ids));
+  c.weights = const_cast<float*>(static_cast<const float*>(weights));
   c.gate_up = static_cast<const u32x4*>(gate_up);
   c.gate_up_scales = static_cast<const _Float16*>(gate_up_scales);
   c.down = static_cast<const u32x4*>(down);
@@ -491,6 +731,8 @@ MoeCall make_call(const void* X, const void* ids, const void* weights, const voi
   c.Y = static_cast<_Float16*>(Y);
   c.hi = reinterpret_cast<_Float16*>(ws + w.hi);
   c.lo = reinterpret_cast<_Float16*>(ws + w.lo);
+  c.part = reinterpret_cast<float*>(ws + w.part);
+  c.counters = reinterpret_cast<unsigned*>(ws + w.counters);
   c.s = MoeShape{static_cast<int>(T), static_cast<int>(E), static_cast<int>(k), static_cast<int>(H), static_cast<int>(I)};
   c.stream = static_cast<hipStream_t>(stream);
   return c;
@@ -502,7 +744,7 @@ extern "C" {
 
 size_t fpx_moe_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I) {
   if (!moe_sizes_ok(T, E, top_k, H, I) || T == 0) return 0;
-  return workspace_of(T, E, top_k, I).bytes;
+  return workspace_of(T, E, top_k, H, I).bytes;
 }
 
 int fpx_moe_experts(int format, const void* X, const void* ids, const void* weights, const void* gate_up,
@@ -533,6 +775,7 @@ int fpx_moe_layer(int format, const void* X, const void* router, const void* gat
   const _Float16* R = static_cast<const _Float16*>(router);
   st = T <= 4 ? launch_logits<1>(c.X, R, logits, c.s, c.stream) : launch_logits<4>(c.X, R, logits, c.s, c.stream);
   if (st != FP6_OK) return st;
+  if (T <= kFusedT && E <= kFusedE) return launch_experts_format(format, c, logits, renormalize);
   int* oi = static_cast<int*>(ids);
   float* ow = static_cast<float*>(weights);
   int E32 = c.s.E, k32 = c.s.k;
