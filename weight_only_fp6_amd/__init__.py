@@ -124,6 +124,8 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 lib = _lib
 
+import torch  # noqa: E402  (after the library's own order of loading, see _load)
+
 
 def _check(func: str, status: int) -> None:
     if status != FP6_OK:
@@ -375,51 +377,40 @@ def sparse_dequant(packed, scales, N: int, K: int, out=None, stream=None):
 
 # ---------------------------------------------------------------------------
 # 8-bit integer linear layer and mixture-of-experts layer.  These calls launch
-# kernels of a few microseconds, so their checks are written out instead of
-# going through _check_device_tensors, and they run on the device and (by
-# default) the current stream of their first tensor.
+# kernels of a few microseconds, so the way to the launch is kept short: checks
+# are one expression per tensor, and the work runs on the device and (by
+# default) the current stream of the first tensor without a context manager
+# where that device is current already.
 # ---------------------------------------------------------------------------
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
 
 
-def _gpu_tensor(t, dtype, shape, device, what: str) -> int:
-    """The address of a contiguous tensor of that dtype and shape on `device`
-    (None: any GPU), else ValueError."""
-    import torch
+def _gpu_tensor(t, dtype, shape, index: int, what: str) -> int:
+    """The address of a contiguous tensor of that dtype and shape on GPU `index`, else ValueError."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index >= 0:
+            return t.data_ptr()
+    except (AttributeError, TypeError, RuntimeError):
+        pass
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{what} must be on the GPU" + (f" {device}, as the first argument" if device else ""))
-    return t.data_ptr()
+    raise ValueError(f"{what} must be on the GPU" + (f", on cuda:{index} as the first argument" if index >= 0 else ""))
 
 
-class _Launch:
-    """Device and stream of one call: makes `device` current and, where the
-    caller gave a stream, makes that current too, so that outputs and workspaces
-    belong to the stream that uses them."""
-
-    def __init__(self, device, stream):
-        import torch
-        self._scopes = []
-        if device.index != torch.cuda.current_device():
-            self._scopes.append(torch.cuda.device(device))
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-            self._scopes.append(torch.cuda.stream(stream))
-        self._device = device
-
-    def __enter__(self):
-        import torch
-        for s in self._scopes:
-            s.__enter__()
-        return torch.cuda.current_stream(self._device).cuda_stream
-
-    def __exit__(self, *exc):
-        for s in reversed(self._scopes):
-            s.__exit__(*exc)
+def _launch(index: int, stream, call):
+    """call(hipStream_t) with GPU `index` current and `stream` (None: the current one), so that
+    outputs and workspaces made inside belong to the stream that uses them."""
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        if stream is None:
+            return call(torch.cuda.current_stream(index).cuda_stream)
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def int8_padded_k(K: int) -> int:
@@ -442,7 +433,6 @@ def int8_quantize_rows(W: np.ndarray):
 
 def _token_rows(X):
     """dtype id, row stride and address of fp16/bf16 rows [M,K] whose elements lie side by side."""
-    import torch
     if not isinstance(X, torch.Tensor) or X.dim() != 2 or X.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("X must be an fp16 or bf16 [M,K] tensor")
     M, K = X.shape
@@ -452,26 +442,27 @@ def _token_rows(X):
         sm = K
     _need(sm >= K, "rows of X must not overlap")
     _need(X.is_cuda, "X must be on the GPU")
-    return (0 if X.dtype == torch.float16 else 1), sm, X.data_ptr()
+    return (0 if X.dtype is torch.float16 else 1), sm, X.data_ptr()
 
 
 def int8_quantize_tokens(X, out=None, scales=None, stream=None):
     """fp16/bf16 [M,K] -> (codes int8 [M,Kp], zero from K on; scales float32 [M]), one scale
     per row: q = RNE(127 x / max|x|).  Rows of X may be a part of wider ones."""
-    import torch
     dt, ldx, px = _token_rows(X)
     M, K = X.shape
     kp = int8_padded_k(K)
     _need(kp > 0, f"K = {K} is out of range")
-    with _Launch(X.device, stream) as s:
-        if out is None:
-            out = torch.empty((M, kp), dtype=torch.int8, device=X.device)
-        if scales is None:
-            scales = torch.empty((M,), dtype=torch.float32, device=X.device)
-        pq = _gpu_tensor(out, torch.int8, (M, kp), X.device, "out")
-        ps = _gpu_tensor(scales, torch.float32, (M,), X.device, "scales")
-        _check("fp6_int8_quantize_tokens", _lib.fp6_int8_quantize_tokens(dt, px, ldx, M, K, pq, ps, s))
-    return out, scales
+    index = X.get_device()
+
+    def call(s):
+        q = torch.empty((M, kp), dtype=torch.int8, device=X.device) if out is None else out
+        sc = torch.empty((M,), dtype=torch.float32, device=X.device) if scales is None else scales
+        _check("fp6_int8_quantize_tokens",
+               _lib.fp6_int8_quantize_tokens(dt, px, ldx, M, K, _gpu_tensor(q, torch.int8, (M, kp), index, "out"),
+                                             _gpu_tensor(sc, torch.float32, (M,), index, "scales"), s))
+        return q, sc
+
+    return _launch(index, stream, call)
 
 
 def int8_linear(X, W, w_scales, x_scales=None, bias=None, out=None, out_dtype=None, stream=None):
@@ -482,24 +473,33 @@ def int8_linear(X, W, w_scales, x_scales=None, bias=None, out=None, out_dtype=No
     float32 [N].  Y and bias [N] are fp16 or bf16: ``out``'s dtype, else ``out_dtype``, else X's
     (codes: fp16).
     """
-    import torch
+    return _int8_product(X, W, w_scales, x_scales, bias, out, out_dtype, stream, 0)
+
+
+def int8_linear_plan(X, W, w_scales, x_scales, variant: int, bias=None, out=None, out_dtype=None, stream=None):
+    """:func:`int8_linear` of int8 codes with the kernel forced (see ``fp6_int8_linear_plan``)."""
+    _need(x_scales is not None, "a forced kernel takes codes")
+    return _int8_product(X, W, w_scales, x_scales, bias, out, out_dtype, stream, variant)
+
+
+def _int8_product(X, W, w_scales, x_scales, bias, out, out_dtype, stream, variant):
     if not isinstance(W, torch.Tensor) or W.dim() != 2:
         raise ValueError("W must be an int8 [N,Kp] tensor")
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError("X must be an int8 [M,Kp] or an fp16 or bf16 [M,K] tensor")
     N, kp = W.shape
     M, K = X.shape
-    codes = X.dtype == torch.int8
-    dev = X.device
+    codes = X.dtype is torch.int8
+    index = X.get_device()
     if codes:
         _need(x_scales is not None, "codes need x_scales")
-        px = _gpu_tensor(X, torch.int8, (M, kp), None, "X")
-        psx = _gpu_tensor(x_scales, torch.float32, (M,), dev, "x_scales")
-        _need(kp % 16 == 0 and 16 <= kp == int8_padded_k(kp), f"Kp = {kp} is not the size of a padded code row")
+        px = _gpu_tensor(X, torch.int8, (M, kp), index, "X")
+        psx = _gpu_tensor(x_scales, torch.float32, (M,), index, "x_scales")
+        _need(kp % 16 == 0 and kp > 0, f"Kp = {kp} is not the size of a padded code row")
     else:
         _need(x_scales is None, "x_scales belong to int8 codes")
         dt, ldx, px = _token_rows(X)
-        _need(0 < kp == int8_padded_k(K), f"W must have {int8_padded_k(K)} codes in a row for K = {K}, got {kp}")
+        _need(kp == (K + 15) // 16 * 16, f"W must have {(K + 15) // 16 * 16} codes in a row for K = {K}, got {kp}")
     if out is not None:
         _need(isinstance(out, torch.Tensor), "out must be a tensor")
         _need(out_dtype is None or out_dtype == out.dtype, "out has another dtype than out_dtype")
@@ -507,44 +507,25 @@ def int8_linear(X, W, w_scales, x_scales=None, bias=None, out=None, out_dtype=No
     elif out_dtype is None:
         out_dtype = torch.float16 if codes else X.dtype
     _need(out_dtype in (torch.float16, torch.bfloat16), "the output is fp16 or bf16")
-    od = 0 if out_dtype == torch.float16 else 1
-    pw = _gpu_tensor(W, torch.int8, (N, kp), dev, "W")
-    psw = _gpu_tensor(w_scales, torch.float32, (N,), dev, "w_scales")
-    pb = 0 if bias is None else _gpu_tensor(bias, out_dtype, (N,), dev, "bias")
-    with _Launch(dev, stream) as s:
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        py = _gpu_tensor(out, out_dtype, (M, N), dev, "out")
+    od = 0 if out_dtype is torch.float16 else 1
+    pw = _gpu_tensor(W, torch.int8, (N, kp), index, "W")
+    psw = _gpu_tensor(w_scales, torch.float32, (N,), index, "w_scales")
+    pb = 0 if bias is None else _gpu_tensor(bias, out_dtype, (N,), index, "bias")
+
+    def call(s):
+        y = torch.empty((M, N), dtype=out_dtype, device=X.device) if out is None else out
+        py = _gpu_tensor(y, out_dtype, (M, N), index, "out")
         if codes:
-            st = _lib.fp6_int8_linear(px, psx, pw, psw, pb, od, py, M, N, kp, s)
+            _check("fp6_int8_linear_plan",
+                   _lib.fp6_int8_linear_plan(px, psx, pw, psw, pb, od, py, M, N, kp, variant, s))
         else:
             nbytes = M * kp + 4 * M
-            ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
-            st = _lib.fp6_int8_linear_tokens(dt, px, ldx, pw, psw, pb, od, py, M, N, K, ws.data_ptr(), nbytes, s)
-        _check("fp6_int8_linear" if codes else "fp6_int8_linear_tokens", st)
-    return out
+            ws = torch.empty((nbytes,), dtype=torch.uint8, device=X.device)
+            _check("fp6_int8_linear_tokens",
+                   _lib.fp6_int8_linear_tokens(dt, px, ldx, pw, psw, pb, od, py, M, N, K, ws.data_ptr(), nbytes, s))
+        return y
 
-
-def int8_linear_plan(X, W, w_scales, x_scales, variant: int, bias=None, out=None, out_dtype=None, stream=None):
-    """:func:`int8_linear` of int8 codes with the kernel forced (see ``fp6_int8_linear_plan``)."""
-    import torch
-    if not isinstance(X, torch.Tensor) or X.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
-        raise ValueError("X must be an int8 [M,Kp] and W an int8 [N,Kp] tensor")
-    (M, kp), N, dev = X.shape, W.shape[0], X.device
-    dtype = out.dtype if out is not None else out_dtype or torch.float16
-    _need(dtype in (torch.float16, torch.bfloat16), "the output is fp16 or bf16")
-    px, pw = _gpu_tensor(X, torch.int8, (M, kp), None, "X"), _gpu_tensor(W, torch.int8, (N, kp), dev, "W")
-    psx = _gpu_tensor(x_scales, torch.float32, (M,), dev, "x_scales")
-    psw = _gpu_tensor(w_scales, torch.float32, (N,), dev, "w_scales")
-    pb = 0 if bias is None else _gpu_tensor(bias, dtype, (N,), dev, "bias")
-    with _Launch(dev, stream) as s:
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype, device=dev)
-        py = _gpu_tensor(out, dtype, (M, N), dev, "out")
-        _check("fp6_int8_linear_plan",
-               _lib.fp6_int8_linear_plan(px, psx, pw, psw, pb, 0 if dtype == torch.float16 else 1, py, M, N, kp,
-                                         variant, s))
-    return out
+    return _launch(index, stream, call)
 
 
 def moe_prepack(codes: np.ndarray, scales: np.ndarray, fmt: str = "e3m2") -> np.ndarray:
@@ -570,7 +551,6 @@ def moe_prepack(codes: np.ndarray, scales: np.ndarray, fmt: str = "e3m2") -> np.
 
 def _moe_args(X, gate_up, gate_up_scales, down, down_scales, fmt):
     """Sizes and addresses of the experts of a call: (format, T, E, H, I, x, gate_up, scales, down, scales)."""
-    import torch
     f = _fmt_id(fmt)
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError("X must be an fp16 [T,H] tensor")
@@ -578,14 +558,18 @@ def _moe_args(X, gate_up, gate_up_scales, down, down_scales, fmt):
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
             raise ValueError(f"{what} must be an fp16 tensor with a row for each expert")
     T, H = X.shape
-    E, I = gate_up_scales.shape[0], gate_up_scales.shape[1] // 2
-    f16, dev = torch.float16, X.device
-    nbytes = packed_bytes(H, I, fmt)
-    return (f, T, E, H, I, _gpu_tensor(X, f16, (T, H), None, "X"),
-            _gpu_tensor(gate_up, torch.uint8, (E, packed_bytes(2 * I, H, fmt)), dev, "gate_up (the moe_prepack output)"),
-            _gpu_tensor(gate_up_scales, f16, (E, 2 * I), dev, "gate_up_scales"),
-            _gpu_tensor(down, torch.uint8, (E, nbytes), dev, "down (the moe_prepack output)"),
-            _gpu_tensor(down_scales, f16, (E, H), dev, "down_scales"))
+    E, I = gate_up_scales.shape
+    I //= 2
+    index = X.get_device()
+    nbytes = H * I * _FORMAT_BITS[f] // 8  # of the down projection; gate_up has twice as many
+    return (f, T, E, H, I, _gpu_tensor(X, torch.float16, (T, H), index, "X"),
+            _gpu_tensor(gate_up, torch.uint8, (E, 2 * nbytes), index, "gate_up (the moe_prepack output)"),
+            _gpu_tensor(gate_up_scales, torch.float16, (E, 2 * I), index, "gate_up_scales"),
+            _gpu_tensor(down, torch.uint8, (E, nbytes), index, "down (the moe_prepack output)"),
+            _gpu_tensor(down_scales, torch.float16, (E, H), index, "down_scales"))
+
+
+_FORMAT_BITS = (6, 6, 5, 4)  # bits(fmt) by format id
 
 
 def moe_experts(X, ids, weights, gate_up, gate_up_scales, down, down_scales, fmt: str = "e3m2", out=None,
@@ -595,22 +579,23 @@ def moe_experts(X, ids, weights, gate_up, gate_up_scales, down, down_scales, fmt
     ids int32 [T,top_k] (outside [0,E): that choice is not served here), weights float32 [T,top_k];
     gate_up and down: :func:`moe_prepack` of [E,2I,H] (gate rows, then up rows) and [E,H,I].
     """
-    import torch
     f, T, E, H, I, px, pg, pgs, pd, pds = _moe_args(X, gate_up, gate_up_scales, down, down_scales, fmt)
-    dev = X.device
+    index = X.get_device()
     _need(isinstance(ids, torch.Tensor) and ids.dim() == 2, "ids must be an int32 [T,top_k] tensor")
     k = ids.shape[1]
-    pi = _gpu_tensor(ids, torch.int32, (T, k), dev, "ids")
-    pw = _gpu_tensor(weights, torch.float32, (T, k), dev, "weights")
-    with _Launch(dev, stream) as s:
-        if out is None:
-            out = torch.empty((T, H), dtype=torch.float16, device=dev)
-        py = _gpu_tensor(out, torch.float16, (T, H), dev, "out")
+    pi = _gpu_tensor(ids, torch.int32, (T, k), index, "ids")
+    pw = _gpu_tensor(weights, torch.float32, (T, k), index, "weights")
+
+    def call(s):
+        y = torch.empty((T, H), dtype=torch.float16, device=X.device) if out is None else out
+        py = _gpu_tensor(y, torch.float16, (T, H), index, "out")
         nbytes = _lib.fpx_moe_workspace_bytes(T, E, k, H, I)
-        ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        ws = torch.empty((nbytes,), dtype=torch.uint8, device=X.device)
         _check("fpx_moe_experts", _lib.fpx_moe_experts(f, px, pi, pw, pg, pgs, pd, pds, py, T, E, k, H, I,
                                                        ws.data_ptr(), nbytes, s))
-    return out
+        return y
+
+    return _launch(index, stream, call)
 
 
 def moe_layer(X, router, gate_up, gate_up_scales, down, down_scales, top_k: int, renormalize: bool = True,
@@ -621,16 +606,16 @@ def moe_layer(X, router, gate_up, gate_up_scales, down, down_scales, top_k: int,
     index; weights are the softmax over all experts, divided by the chosen ones' sum where
     ``renormalize``.  The experts are those of :func:`moe_experts`.
     """
-    import torch
     f, T, E, H, I, px, pg, pgs, pd, pds = _moe_args(X, gate_up, gate_up_scales, down, down_scales, fmt)
-    dev = X.device
-    pr = _gpu_tensor(router, torch.float16, (E, H), dev, "router")
+    index = X.get_device()
+    pr = _gpu_tensor(router, torch.float16, (E, H), index, "router")
     k = int(top_k)
     _need(1 <= k <= E, f"top_k = {k} is not in 1 .. {E}")
-    with _Launch(dev, stream) as s:
-        if out is None:
-            out = torch.empty((T, H), dtype=torch.float16, device=dev)
-        py = _gpu_tensor(out, torch.float16, (T, H), dev, "out")
+
+    def call(s):
+        dev = X.device
+        y = torch.empty((T, H), dtype=torch.float16, device=dev) if out is None else out
+        py = _gpu_tensor(y, torch.float16, (T, H), index, "out")
         ids = torch.empty((T, k), dtype=torch.int32, device=dev)
         weights = torch.empty((T, k), dtype=torch.float32, device=dev)
         nbytes = _lib.fpx_moe_workspace_bytes(T, E, k, H, I)
@@ -638,7 +623,9 @@ def moe_layer(X, router, gate_up, gate_up_scales, down, down_scales, top_k: int,
         _check("fpx_moe_layer", _lib.fpx_moe_layer(f, px, pr, pg, pgs, pd, pds, 1 if renormalize else 0, py,
                                                    ids.data_ptr(), weights.data_ptr(), T, E, k, H, I,
                                                    ws.data_ptr(), nbytes, s))
-    return out, ids, weights
+        return y, ids, weights
+
+    return _launch(index, stream, call)
 
 
 def release() -> None:

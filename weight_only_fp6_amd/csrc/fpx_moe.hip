@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "fp6_limits.h"
+#include "fpx_cus.h"
 #include "fpx_device.h"
 #include "fpx_moe.h"
 
@@ -604,14 +605,6 @@ Split choose_split(int64_t row_blocks, int64_t ktiles, int64_t slots, int cus) {
   return s;
 }
 
-int device_cus() {
-  int dev = 0, cus = 0;
-  if (hipGetDevice(&dev) != hipSuccess ||
-      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-    cus = 256;
-  return cus;
-}
-
 // logits: of fpx_moe_layer, whose choice is not made yet (then the first
 // product makes it); null: ids and weights are there.
 template <int F>
@@ -622,7 +615,7 @@ int launch_experts(const MoeCall& c, const double* logits, int renorm) {
   int by_pair = group_tokens * s.k < s.E;
   int slots = by_pair ? group_tokens * s.k : s.E;
   const unsigned grid_y = static_cast<unsigned>(slots) * static_cast<unsigned>(fpx_ceil_div(group_tokens, 16));
-  const int cus = device_cus();
+  const int cus = fpx::current_cus();
   const _Float16* X = c.X;
   int* ids = c.ids;
   float* weights = c.weights;

@@ -9,6 +9,7 @@
 
 #include "fp6_int8.h"
 #include "fp6_limits.h"
+#include "fpx_cus.h"
 
 namespace {
 
@@ -584,14 +585,6 @@ int choose_variant(const Product& p, int cus) {
   return best;
 }
 
-int device_cus() {
-  int dev = 0, cus = 0;
-  if (hipGetDevice(&dev) != hipSuccess ||
-      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-    cus = 256;
-  return cus;
-}
-
 template <int DT>
 int launch_product_t(const Product& p, int variant, hipStream_t s) {
   switch (variant) {  // WA, WB, TA, TB, D, WK
@@ -610,7 +603,7 @@ int launch_product_t(const Product& p, int variant, hipStream_t s) {
 }
 
 int launch_product(int dtype, const Product& p, int variant, hipStream_t s) {
-  if (variant == kAuto) variant = choose_variant(p, device_cus());
+  if (variant == kAuto) variant = choose_variant(p, fpx::current_cus());
   return dtype == FP6_FP16 ? launch_product_t<FP6_FP16>(p, variant, s) : launch_product_t<FP6_BF16>(p, variant, s);
 }
 
