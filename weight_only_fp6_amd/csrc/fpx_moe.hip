@@ -29,13 +29,11 @@ constexpr int kMaxE = static_cast<int>(fp6::kMoeMaxExperts);
 constexpr float kHScale = 0x1p-8f, kLoScale = 0x1p11f;
 
 constexpr int kFusedE = 128, kFusedT = 4;  // sizes up to which the choice is made inside the first product
+constexpr int kFewPairs = 64, kFewTiles = 32;  // moe_down_few: a lane per pair, two tiles per wave
 
 struct MoeShape {
   int T, E, k, H, I;
 };
-
-// Row groups of the second product, at most (one row block each): its counters.
-__host__ __device__ constexpr int row_groups(int64_t H) { return static_cast<int>(H / 16); }
 
 // ---------------------------------------------------------------------------
 // Router logits in 64 bits.  A product of two fp16 numbers is exact in fp32,
@@ -141,8 +139,8 @@ __global__ __launch_bounds__(64) void moe_topk(const double* __restrict__ logits
 }
 
 // ---------------------------------------------------------------------------
-// Both products give a workgroup of 4 waves one expert, up to 16 of its tokens
-// (the columns of the MFMAs) and (4/ks)*P row blocks of 16 rows: ks waves split
+// Both products give a workgroup of 4 waves one expert, its tokens, 16 at a time
+// (the columns of the MFMAs), and (4/ks)*P row blocks of 16 rows: ks waves split
 // K, each takes P consecutive row blocks and holds a k-tile's token fragments
 // for all of them.  The weights run through a register ring of D k-tiles: as
 // soon as tile (row block p, k-tile t) is multiplied, tile (p, t+D) is
@@ -151,8 +149,10 @@ __global__ __launch_bounds__(64) void moe_topk(const double* __restrict__ logits
 //
 // Which expert: with fewer (token, choice) pairs than experts the grid has one
 // slot per pair, and the first pair of an expert takes it; else one slot per
-// expert.  Experts with more than 16 tokens have further workgroups, one per 16
-// tokens.  Workgroups without work leave at once.
+// expert.  Workgroups without work leave at once.  (Further workgroups for an
+// expert's tokens behind the 16th, most of them without work, cost 15 of 50 us
+// at 64 tokens and 64 experts; the workgroup goes over its weights again
+// instead, from the L2 or the 256 MB cache.)
 //
 // A wave's lane is a token of the group here: `first` is its first choice of
 // the expert (pair index inside the group, -1: none), `weight` the sum of the
@@ -188,26 +188,38 @@ __device__ __forceinline__ Choice choice_of(const int* __restrict__ ids, const f
   return c;
 }
 
-// Whether this workgroup has work: mask of the expert's tokens, its chunk of 16
-// of them, and (slots by pair) whether the slot's pair is the expert's first.
-__device__ __forceinline__ bool has_work(uint64_t mask, int first, int chunk, int by_pair, int slot) {
-  if (16 * chunk >= __popcll(mask)) return false;
+// Whether this workgroup has work: any token chose its expert, and (slots by
+// pair) the slot's pair is the expert's first.
+__device__ __forceinline__ bool has_work(uint64_t mask, int first, int by_pair, int slot) {
+  if (mask == 0) return false;
   if (!by_pair) return true;
   return __builtin_amdgcn_readlane(first, __ffsll(static_cast<unsigned long long>(mask)) - 1) == slot;
+}
+
+// h = w * silu(gate) * up of 4 rows, as its two halves.
+__device__ __forceinline__ void store_gated(_Float16* hi, _Float16* lo, const float4v& gate, const float4v& up, float w) {
+  half4v oh, ol;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float h = (gate[i] / (1.0f + expf(-gate[i]))) * up[i] * w * kHScale;
+    oh[i] = static_cast<_Float16>(h);
+    const float hf = static_cast<float>(oh[i]);
+    ol[i] = __builtin_isinf(hf) ? static_cast<_Float16>(0.0f) : static_cast<_Float16>((h - hf) * kLoScale);
+  }
+  *reinterpret_cast<half4v*>(hi) = oh;
+  *reinterpret_cast<half4v*>(lo) = ol;
 }
 
 // Gate and up products with the gated activation; row block p of the gate and
 // of the up projection go together.  FUSED (few tokens, few experts): the
 // choice is made here from the logits, wave t for token t, by every workgroup
-// for itself, and written out by the first one.  The first workgroup also clears
-// the counters of the second product.
+// for itself, and written out by the first one.
 template <int F, int P, int D, bool FUSED>
-__global__ __launch_bounds__(256) void moe_gate_up(const _Float16* __restrict__ X, const double* __restrict__ logits,
+__global__ __launch_bounds__(256, 2) void moe_gate_up(const _Float16* __restrict__ X, const double* __restrict__ logits,
                                                    int* __restrict__ ids_g, float* __restrict__ weights_g,
                                                    const u32x4* __restrict__ wp, const _Float16* __restrict__ scales,
                                                    _Float16* __restrict__ hi, _Float16* __restrict__ lo,
-                                                   unsigned* __restrict__ counters, MoeShape s, int ks, int by_pair,
-                                                   int slots, int renorm) {
+                                                   MoeShape s, int ks, int by_pair, int renorm) {
   __shared__ short col_token[4][kGroup], col_pair[4][kGroup];
   __shared__ float col_w[4][kGroup];
   __shared__ float4v red[4][2 * P][64];
@@ -221,8 +233,6 @@ __global__ __launch_bounds__(256) void moe_gate_up(const _Float16* __restrict__ 
   const int t0 = blockIdx.z * kGroup;
   const int tokens = s.T - t0 < kGroup ? s.T - t0 : kGroup;
   const bool first_wg = blockIdx.x == 0 && blockIdx.y == 0;
-  if (first_wg && blockIdx.z == 0)
-    for (int i = threadIdx.x; i < row_groups(s.H); i += 256) counters[i] = 0u;
   const int* ids = ids_g + static_cast<int64_t>(t0) * s.k;
   const float* weights = weights_g + static_cast<int64_t>(t0) * s.k;
   if constexpr (FUSED) {
@@ -243,7 +253,7 @@ __global__ __launch_bounds__(256) void moe_gate_up(const _Float16* __restrict__ 
     ids = f_ids;
     weights = f_w;
   }
-  const int chunk = blockIdx.y / slots, slot = blockIdx.y - chunk * slots;
+  const int slot = blockIdx.y;
   int e = slot;
   if (by_pair) {
     if (slot >= tokens * s.k) return;
@@ -262,22 +272,25 @@ __global__ __launch_bounds__(256) void moe_gate_up(const _Float16* __restrict__ 
   typename Fmt<F>::Tile tg[D][P], tu[D][P];
   _Float16 sg[P], su[P];
   const _Float16* sc = scales + static_cast<int64_t>(e) * 2 * s.I + nb * 16 + r;
+  auto load_first = [&]() {
 #pragma unroll
-  for (int d = 0; d < D; ++d) {
-    const int64_t at = (kt0 + d < kt1 ? kt0 + d : kt0) * kstr;
+    for (int d = 0; d < D; ++d) {
+      const int64_t at = (kt0 + d < kt1 ? kt0 + d : kt0) * kstr;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      Fmt<F>::template load<true>(tg[d][p], wg + at + p * Fmt<F>::kTileQuads, lane);
-      Fmt<F>::template load<true>(tu[d][p], wu + at + p * Fmt<F>::kTileQuads, lane);
+      for (int p = 0; p < P; ++p) {
+        Fmt<F>::template load<true>(tg[d][p], wg + at + p * Fmt<F>::kTileQuads, lane);
+        Fmt<F>::template load<true>(tu[d][p], wu + at + p * Fmt<F>::kTileQuads, lane);
+      }
     }
-  }
+  };
+  load_first();
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     sg[p] = sc[16 * p];
     su[p] = sc[s.I + 16 * p];
   }
   const uint64_t mask = __ballot(ch.first >= 0);
-  if (!has_work(mask, ch.first, chunk, by_pair, slot)) return;
+  if (!has_work(mask, ch.first, by_pair, slot)) return;
   const int n = __popcll(mask);
   if (ch.first >= 0) {
     const int c = __popcll(mask & ((uint64_t(1) << lane) - 1));
@@ -286,8 +299,13 @@ __global__ __launch_bounds__(256) void moe_gate_up(const _Float16* __restrict__ 
     col_w[wave][c] = ch.weight;
   }
   __builtin_amdgcn_wave_barrier();
-  // Column r; columns behind the expert's last token repeat the chunk's first and are not stored.
-  const int c = 16 * chunk + r < n ? 16 * chunk + r : 16 * chunk;
+  for (int c0 = 0; c0 < n; c0 += 16) {
+  if (c0 > 0) {
+    __syncthreads();
+    load_first();
+  }
+  // Column r; columns behind the expert's last token repeat the first of the 16 and are not stored.
+  const int c = c0 + r < n ? c0 + r : c0;
   const _Float16* xr = X + static_cast<int64_t>(t0 + col_token[wave][c]) * s.H + 8 * g;
   half8v xf[2][8];
 #pragma unroll
@@ -336,7 +354,7 @@ __global__ __launch_bounds__(256) void moe_gate_up(const _Float16* __restrict__ 
   }
   __syncthreads();
   // Wave (rb, kslice) sums and stores the row blocks kslice, kslice + ks, ...
-  if (16 * chunk + r < n) {
+  if (c0 + r < n) {
     const int64_t at = (static_cast<int64_t>(t0) * s.k + col_pair[wave][c]) * s.I + nb * 16 + 4 * g;
     const float w = col_w[wave][c];
     for (int p = kslice; p < P; p += ks) {
@@ -345,29 +363,19 @@ __global__ __launch_bounds__(256) void moe_gate_up(const _Float16* __restrict__ 
         vg += red[rb * ks + q][2 * p][lane];
         vu += red[rb * ks + q][2 * p + 1][lane];
       }
-      half4v oh, ol;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float h = (vg[i] / (1.0f + expf(-vg[i]))) * vu[i] * w * kHScale;
-        oh[i] = static_cast<_Float16>(h);
-        const float hf = static_cast<float>(oh[i]);
-        ol[i] = __builtin_isinf(hf) ? static_cast<_Float16>(0.0f) : static_cast<_Float16>((h - hf) * kLoScale);
-      }
-      *reinterpret_cast<half4v*>(hi + at + 16 * p) = oh;
-      *reinterpret_cast<half4v*>(lo + at + 16 * p) = ol;
+      store_gated(hi + at + 16 * p, lo + at + 16 * p, vg, vu, w);
     }
+  }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Down product and the sum over experts.  Every workgroup stores its expert's
-// part of the outputs, one fp32 row per pair (the weight of the choice is
-// already in h); each output adds its token's parts in the order of the choices
-// and is rounded once.  With few tokens (SUM) this happens in the same kernel:
-// parts are stored device-wide, a workgroup counts itself at its row group, and
-// the last one there (none waits for another) adds.  With more, that last
-// workgroup would add for many tokens alone (64 tokens, 64 experts, 2048x1024:
-// 181 us against 52 with a kernel of its own).
+// Down product and the sum over experts, more than a few tokens: a workgroup
+// stores its expert's part of the outputs, one fp32 row per pair (the weight of
+// the choice is already in h), and moe_sum adds each token's parts in the order
+// of its choices and rounds once.  (Letting the last workgroup of a row group
+// add instead of a kernel of its own: 64 tokens, 64 experts 2048x1024 181 us
+// against 37.)
 // ---------------------------------------------------------------------------
 template <typename LOAD>
 __device__ __forceinline__ void sum_choices(const int* __restrict__ ids, const MoeShape& s, LOAD load, _Float16* y) {
@@ -393,152 +401,571 @@ __device__ __forceinline__ void sum_choices(const int* __restrict__ ids, const M
   *reinterpret_cast<half4v*>(y) = o;
 }
 
-template <int F, int P, int D, bool SUM>
-__global__ __launch_bounds__(256) void moe_down(const _Float16* __restrict__ hi, const _Float16* __restrict__ lo,
+template <int F, int P, int D>
+__global__ __launch_bounds__(256, 2) void moe_down(const _Float16* __restrict__ hi, const _Float16* __restrict__ lo,
                                                 const int* __restrict__ ids_g, const u32x4* __restrict__ wp,
-                                                const _Float16* __restrict__ scales, float* __restrict__ part,
-                                                unsigned* __restrict__ counters, _Float16* __restrict__ Y, MoeShape s,
-                                                int ks, int by_pair, int slots) {
+                                                const _Float16* __restrict__ scales, float* __restrict__ part, MoeShape s,
+                                                int ks, int by_pair) {
   __shared__ short col_pair[4][kGroup];
   __shared__ float4v red[4][P][64];
-  __shared__ unsigned arrived;
-  constexpr int kSc1 = 16;                // cache policy: device scope
-  constexpr int kRsrcWord3 = 0x00020000;  // raw 32-bit buffer, gfx9 family
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int t0 = blockIdx.z * kGroup;
   const int tokens = s.T - t0 < kGroup ? s.T - t0 : kGroup;
   const int* ids = ids_g + static_cast<int64_t>(t0) * s.k;
-  const int chunk = blockIdx.y / slots, slot = blockIdx.y - chunk * slots;
+  const int slot = blockIdx.y;
   const int rows0 = blockIdx.x * (4 / ks) * P * 16;  // this workgroup's rows of the output
   float* parts = part + static_cast<int64_t>(t0) * s.k * s.H;
-  [[maybe_unused]] __amdgpu_buffer_rsrc_t rsrc;  // SUM: at most 4 tokens' parts, below 2^31 bytes
-  if constexpr (SUM)
-    rsrc = __builtin_amdgcn_make_buffer_rsrc(parts, static_cast<short>(0), tokens * s.k * s.H * 4, kRsrcWord3);
 
   int e = slot;
-  bool work = true;
   if (by_pair) {
-    work = slot < tokens * s.k;
-    if (work) {
-      e = __builtin_amdgcn_readfirstlane(ids[slot]);
-      work = e >= 0 && e < s.E;
-    }
+    if (slot >= tokens * s.k) return;
+    e = __builtin_amdgcn_readfirstlane(ids[slot]);
+    if (e < 0 || e >= s.E) return;
   }
-  if (work) {
-    const Choice ch = choice_of<false>(ids, nullptr, tokens, s.k, e, lane);
-    const int rb = wave / ks, kslice = wave - rb * ks;
-    const int ktiles = s.I >> 8;
-    const int nb = (blockIdx.x * (4 / ks) + rb) * P;
-    const int64_t kstr = static_cast<int64_t>(s.H >> 4) * Fmt<F>::kTileQuads;
-    const u32x4* w = wp + static_cast<int64_t>(e) * ktiles * kstr + nb * static_cast<int64_t>(Fmt<F>::kTileQuads) + lane;
-    const int kt0 = kslice * ktiles / ks, kt1 = (kslice + 1) * ktiles / ks;
-    typename Fmt<F>::Tile tw[D][P];
-    _Float16 sw[P];
-    const _Float16* sc = scales + static_cast<int64_t>(e) * s.H + nb * 16 + r;
+  const Choice ch = choice_of<false>(ids, nullptr, tokens, s.k, e, lane);
+  const int rb = wave / ks, kslice = wave - rb * ks;
+  const int ktiles = s.I >> 8;
+  const int nb = (blockIdx.x * (4 / ks) + rb) * P;
+  const int64_t kstr = static_cast<int64_t>(s.H >> 4) * Fmt<F>::kTileQuads;
+  const u32x4* w = wp + static_cast<int64_t>(e) * ktiles * kstr + nb * static_cast<int64_t>(Fmt<F>::kTileQuads) + lane;
+  const int kt0 = kslice * ktiles / ks, kt1 = (kslice + 1) * ktiles / ks;
+  typename Fmt<F>::Tile tw[D][P];
+  _Float16 sw[P];
+  const _Float16* sc = scales + static_cast<int64_t>(e) * s.H + nb * 16 + r;
+  auto load_first = [&]() {
 #pragma unroll
     for (int d = 0; d < D; ++d)
 #pragma unroll
       for (int p = 0; p < P; ++p)
         Fmt<F>::template load<true>(tw[d][p], w + (kt0 + d < kt1 ? kt0 + d : kt0) * kstr + p * Fmt<F>::kTileQuads, lane);
+  };
+  load_first();
 #pragma unroll
-    for (int p = 0; p < P; ++p) sw[p] = sc[16 * p];
-    const uint64_t mask = __ballot(ch.first >= 0);
-    work = has_work(mask, ch.first, chunk, by_pair, slot);
-    if (work) {
-      const int n = __popcll(mask);
-      if (ch.first >= 0) col_pair[wave][__popcll(mask & ((uint64_t(1) << lane) - 1))] = static_cast<short>(ch.first);
-      __builtin_amdgcn_wave_barrier();
-      const int c = 16 * chunk + r < n ? 16 * chunk + r : 16 * chunk;
-      const int pair = col_pair[wave][c];
-      const int64_t at = (static_cast<int64_t>(t0) * s.k + pair) * s.I + 8 * g;
-      const _Float16 *hr = hi + at, *lr = lo + at;
-      half8v fh[2][8], fl[2][8];
+  for (int p = 0; p < P; ++p) sw[p] = sc[16 * p];
+  const uint64_t mask = __ballot(ch.first >= 0);
+  if (!has_work(mask, ch.first, by_pair, slot)) return;
+  const int n = __popcll(mask);
+  if (ch.first >= 0) col_pair[wave][__popcll(mask & ((uint64_t(1) << lane) - 1))] = static_cast<short>(ch.first);
+  __builtin_amdgcn_wave_barrier();
+  for (int c0 = 0; c0 < n; c0 += 16) {
+  if (c0 > 0) {
+    __syncthreads();
+    load_first();
+  }
+  const int c = c0 + r < n ? c0 + r : c0;
+  const int pair = col_pair[wave][c];
+  const int64_t at = (static_cast<int64_t>(t0) * s.k + pair) * s.I + 8 * g;
+  const _Float16 *hr = hi + at, *lr = lo + at;
+  half8v fh[2][8], fl[2][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        fh[0][j] = *reinterpret_cast<const half8v*>(hr + kt0 * 256 + 32 * j);
-        fl[0][j] = *reinterpret_cast<const half8v*>(lr + kt0 * 256 + 32 * j);
-      }
-      float4v ah[P], al[P];
+  for (int j = 0; j < 8; ++j) {
+    fh[0][j] = *reinterpret_cast<const half8v*>(hr + kt0 * 256 + 32 * j);
+    fl[0][j] = *reinterpret_cast<const half8v*>(lr + kt0 * 256 + 32 * j);
+  }
+  float4v ah[P], al[P];
 #pragma unroll
-      for (int p = 0; p < P; ++p) ah[p] = al[p] = float4v{0.f, 0.f, 0.f, 0.f};
-      auto tile = [&](int kt, auto CUR) {
-        constexpr int cur = decltype(CUR)::value;
-        const int next = kt + 1 < kt1 ? kt + 1 : kt;  // behind the end: a stand-in
+  for (int p = 0; p < P; ++p) ah[p] = al[p] = float4v{0.f, 0.f, 0.f, 0.f};
+  auto tile = [&](int kt, auto CUR) {
+    constexpr int cur = decltype(CUR)::value;
+    const int next = kt + 1 < kt1 ? kt + 1 : kt;  // behind the end: a stand-in
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          fh[1 - cur][j] = *reinterpret_cast<const half8v*>(hr + next * 256 + 32 * j);
-          fl[1 - cur][j] = *reinterpret_cast<const half8v*>(lr + next * 256 + 32 * j);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+    for (int j = 0; j < 8; ++j) {
+      fh[1 - cur][j] = *reinterpret_cast<const half8v*>(hr + next * 256 + 32 * j);
+      fl[1 - cur][j] = *reinterpret_cast<const half8v*>(lr + next * 256 + 32 * j);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const half2v s2 = scale2_of<F>(sw[p]);
-          auto step = [&](auto J) {
-            constexpr int j = decltype(J)::value;
-            const half8v a = Fmt<F>::template step<j>(tw[cur % D][p], s2);
-            ah[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fh[cur][j], ah[p], 0, 0, 0);
-            al[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fl[cur][j], al[p], 0, 0, 0);
-          };
-          step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
-          step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
-          step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
-          step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
-          __builtin_amdgcn_sched_barrier(0);
-          if (kt + D < kt1)
-            Fmt<F>::template load<true>(tw[cur % D][p], w + (kt + D) * kstr + p * Fmt<F>::kTileQuads, lane);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+    for (int p = 0; p < P; ++p) {
+      const half2v s2 = scale2_of<F>(sw[p]);
+      auto step = [&](auto J) {
+        constexpr int j = decltype(J)::value;
+        const half8v a = Fmt<F>::template step<j>(tw[cur % D][p], s2);
+        ah[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fh[cur][j], ah[p], 0, 0, 0);
+        al[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fl[cur][j], al[p], 0, 0, 0);
       };
-      int kt = kt0;
-      for (; kt + 2 <= kt1; kt += 2) {
-        tile(kt, std::integral_constant<int, 0>{});
-        tile(kt + 1, std::integral_constant<int, 1>{});
-      }
-      if (kt < kt1) tile(kt, std::integral_constant<int, 0>{});
+      step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
+      step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
+      step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
+      step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
+      __builtin_amdgcn_sched_barrier(0);
+      if (kt + D < kt1)
+        Fmt<F>::template load<true>(tw[cur % D][p], w + (kt + D) * kstr + p * Fmt<F>::kTileQuads, lane);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  int kt = kt0;
+  for (; kt + 2 <= kt1; kt += 2) {
+    tile(kt, std::integral_constant<int, 0>{});
+    tile(kt + 1, std::integral_constant<int, 1>{});
+  }
+  if (kt < kt1) tile(kt, std::integral_constant<int, 0>{});
 #pragma unroll
-      for (int p = 0; p < P; ++p) red[wave][p][lane] = ah[p] + al[p] * (1.0f / kLoScale);
-      __syncthreads();
-      if (16 * chunk + r < n) {
-        const int64_t dst = static_cast<int64_t>(pair) * s.H + rows0 + rb * P * 16 + 4 * g;
-        for (int p = kslice; p < P; p += ks) {
-          float4v v = red[rb * ks][p][lane];
-          for (int q = 1; q < ks; ++q) v += red[rb * ks + q][p][lane];
-          if constexpr (SUM)
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, static_cast<int>(dst + 16 * p) * 4, 0, kSc1);
-          else
-            *reinterpret_cast<float4v*>(parts + dst + 16 * p) = v;
-        }
-      }
+  for (int p = 0; p < P; ++p) red[wave][p][lane] = ah[p] + al[p] * (1.0f / kLoScale);
+  __syncthreads();
+  if (c0 + r < n) {
+    const int64_t dst = static_cast<int64_t>(pair) * s.H + rows0 + rb * P * 16 + 4 * g;
+    for (int p = kslice; p < P; p += ks) {
+      float4v v = red[rb * ks][p][lane];
+      for (int q = 1; q < ks; ++q) v += red[rb * ks + q][p][lane];
+      *reinterpret_cast<float4v*>(parts + dst + 16 * p) = v;
     }
   }
-  if constexpr (SUM) {
-    __builtin_amdgcn_s_waitcnt(0);  // this wave's parts are stored
-    __syncthreads();
-    if (threadIdx.x == 0)
-      arrived = __hip_atomic_fetch_add(counters + blockIdx.x, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (arrived != gridDim.y - 1) return;
-    const int quads = (4 / ks) * P * 4;  // 16-byte units of the row group
-    for (int i = threadIdx.x; i < tokens * quads; i += 256) {
-      const int t = i / quads, row = rows0 + 4 * (i - t * quads);
-      sum_choices(ids + t * s.k, s, [&](int j) {
-        return __builtin_bit_cast(float4v, __builtin_amdgcn_raw_buffer_load_b128(
-                                               rsrc, ((t * s.k + j) * s.H + row) * 4, 0, kSc1));
-      }, Y + static_cast<int64_t>(t) * s.H + row);
-    }
   }
 }
 
-// Many tokens: the sum in a kernel of its own, 4 rows of a token per thread.
+// ---------------------------------------------------------------------------
+// The same products for many row blocks: the 4 waves of a workgroup take P
+// consecutive row blocks each over the whole K and share the token fragments
+// through LDS, which leaves the registers to a deeper ring of weights (D
+// k-tiles): one wave's fragments of a k-tile are 8 KB (h: 16 KB), more than its
+// weights, and come once per workgroup instead of once per wave.
+//
+// LDS buffer of a k-tile (two of them, filled by direct LDS loads one k-tile
+// ahead): 16 columns x 32 units of 16 bytes, unit u of column c at place
+// u ^ (c % 8), so that eight columns' reads of one unit cover a 128-byte line.
+// Per k-tile: wait for this wave's direct loads (a fixed count of weight loads
+// may still be in flight behind them), barrier, request the next k-tile's
+// columns, multiply, request the weights of k-tile t+D.
+// ---------------------------------------------------------------------------
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+
+// Direct loads of one k-tile of 16 columns by 4 waves: wave w fills units
+// [128 w, 128 w + 128); src[i]: this lane's source of unit 128 w + 64 i + lane.
+__device__ __forceinline__ void load_columns(half8v* buf, const _Float16* const (&src)[2], int kt, int wave) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) lds_load<16>(src[i] + kt * 256, buf + 128 * wave + 64 * i);
+}
+
+template <int F, int P, int D, int NC>
+__global__ __launch_bounds__(256, 2) void moe_gate_up_wide(const _Float16* __restrict__ X, const int* __restrict__ ids_g,
+                                                        const float* __restrict__ weights_g,
+                                                        const u32x4* __restrict__ wp,
+                                                        const _Float16* __restrict__ scales, _Float16* __restrict__ hi,
+                                                        _Float16* __restrict__ lo, MoeShape s, int by_pair) {
+  static_assert(D % 2 == 0, "two column buffers");
+  __shared__ short col_token[4][kGroup], col_pair[4][kGroup];
+  __shared__ float col_w[4][kGroup];
+  __shared__ half8v buf0[512 * NC], buf1[512 * NC];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int t0 = blockIdx.z * kGroup;
+  const int tokens = s.T - t0 < kGroup ? s.T - t0 : kGroup;
+  const int* ids = ids_g + static_cast<int64_t>(t0) * s.k;
+  const int slot = blockIdx.y;
+  int e = slot;
+  if (by_pair) {
+    if (slot >= tokens * s.k) return;
+    e = __builtin_amdgcn_readfirstlane(ids[slot]);
+    if (e < 0 || e >= s.E) return;
+  }
+  const Choice ch = choice_of<true>(ids, weights_g + static_cast<int64_t>(t0) * s.k, tokens, s.k, e, lane);
+  const int iblocks = s.I >> 4, ktiles = s.H >> 8;
+  const int nb = (blockIdx.x * 4 + wave) * P;
+  const int64_t kstr = 2 * static_cast<int64_t>(iblocks) * Fmt<F>::kTileQuads;
+  const u32x4* wg = wp + static_cast<int64_t>(e) * ktiles * kstr + nb * static_cast<int64_t>(Fmt<F>::kTileQuads) + lane;
+  const u32x4* wu = wg + static_cast<int64_t>(iblocks) * Fmt<F>::kTileQuads;
+  _Float16 sg[P], su[P];
+  const _Float16* sc = scales + static_cast<int64_t>(e) * 2 * s.I + nb * 16 + r;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    sg[p] = sc[16 * p];
+    su[p] = sc[s.I + 16 * p];
+  }
+  const uint64_t mask = __ballot(ch.first >= 0);
+  if (!has_work(mask, ch.first, by_pair, slot)) return;
+  const int n = __popcll(mask);
+  if (ch.first >= 0) {
+    const int c = __popcll(mask & ((uint64_t(1) << lane) - 1));
+    col_token[wave][c] = static_cast<short>(lane);
+    col_pair[wave][c] = static_cast<short>(ch.first);
+    col_w[wave][c] = ch.weight;
+  }
+  __builtin_amdgcn_wave_barrier();
+  typename Fmt<F>::Tile tg[D][P], tu[D][P];
+  constexpr int kW = 2 * P * Fmt<F>::kTileLoads;  // weight loads per k-tile
+  auto load_w = [&](int slot_, int kt) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      Fmt<F>::template load<true>(tg[slot_][p], wg + kt * kstr + p * Fmt<F>::kTileQuads, lane);
+      Fmt<F>::template load<true>(tu[slot_][p], wu + kt * kstr + p * Fmt<F>::kTileQuads, lane);
+    }
+  };
+  // One pass: C groups of 16 columns, from column c0 on.
+  auto pass = [&](int c0, auto C) {
+    constexpr int nc = decltype(C)::value;
+    const _Float16* src[nc][2];
+#pragma unroll
+    for (int q = 0; q < nc; ++q)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = 4 * wave + 2 * i + (lane >> 5), c = c0 + 16 * q + col;
+        src[q][i] = X + static_cast<int64_t>(t0 + col_token[wave][c < n ? c : c0]) * s.H + 8 * ((lane & 31) ^ (col & 7));
+      }
+    auto columns = [&](half8v* buf, int kt) {
+#pragma unroll
+      for (int q = 0; q < nc; ++q) load_columns(buf + 512 * q, src[q], kt, wave);
+    };
+    columns(buf0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int d = 0; d < D; ++d) load_w(d, d < ktiles ? d : 0);
+    float4v ag[nc][P], au[nc][P];
+#pragma unroll
+    for (int q = 0; q < nc; ++q)
+#pragma unroll
+      for (int p = 0; p < P; ++p) ag[q][p] = au[q][p] = float4v{0.f, 0.f, 0.f, 0.f};
+    auto tile = [&](int kt, auto U) {
+      constexpr int u = decltype(U)::value;
+      const half8v* cur = u & 1 ? buf1 : buf0;
+      __builtin_amdgcn_sched_barrier(0);
+      // Behind this k-tile's columns: at first all D k-tiles of weights, later
+      // those of k-tile t-1+D, at the end nothing.
+      if (kt == 0) wait_vm<D * kW>();
+      else if (kt - 1 + D < ktiles) wait_vm<kW>();
+      else wait_vm<0>();
+      barrier_no_fence();
+      if (kt + 1 < ktiles) columns(u & 1 ? buf0 : buf1, kt + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      half2v s2g[P], s2u[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        s2g[p] = scale2_of<F>(sg[p]);
+        s2u[p] = scale2_of<F>(su[p]);
+      }
+      auto step = [&](auto J) {
+        constexpr int j = decltype(J)::value;
+        half8v x[nc];
+#pragma unroll
+        for (int q = 0; q < nc; ++q) x[q] = cur[512 * q + r * 32 + ((4 * j + g) ^ (r & 7))];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const half8v a = Fmt<F>::template step<j>(tg[u][p], s2g[p]), b = Fmt<F>::template step<j>(tu[u][p], s2u[p]);
+#pragma unroll
+          for (int q = 0; q < nc; ++q) {
+            ag[q][p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, x[q], ag[q][p], 0, 0, 0);
+            au[q][p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, x[q], au[q][p], 0, 0, 0);
+          }
+        }
+      };
+      step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
+      step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
+      step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
+      step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
+      __builtin_amdgcn_sched_barrier(0);
+      if (kt + D < ktiles) load_w(u, kt + D);
+    };
+    for (int kt = 0; kt < ktiles; kt += D) {
+      tile(kt, std::integral_constant<int, 0>{});
+      if (kt + 1 < ktiles) tile(kt + 1, std::integral_constant<int, 1>{});
+      if constexpr (D > 2) {
+        if (kt + 2 < ktiles) tile(kt + 2, std::integral_constant<int, 2>{});
+        if (kt + 3 < ktiles) tile(kt + 3, std::integral_constant<int, 3>{});
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < nc; ++q) {
+      const int c = c0 + 16 * q + r;
+      if (c < n) {
+        const int64_t at = (static_cast<int64_t>(t0) * s.k + col_pair[wave][c]) * s.I + nb * 16 + 4 * g;
+#pragma unroll
+        for (int p = 0; p < P; ++p) store_gated(hi + at + 16 * p, lo + at + 16 * p, ag[q][p], au[q][p], col_w[wave][c]);
+      }
+    }
+  };
+  if constexpr (NC == 2) {
+    int c0 = 0;
+    for (; n - c0 > 16; c0 += 32) {
+      pass(c0, std::integral_constant<int, 2>{});
+      __syncthreads();  // the buffers are free again
+    }
+    if (c0 < n) pass(c0, std::integral_constant<int, 1>{});
+  } else {
+    pass(0, std::integral_constant<int, 1>{});  // at most 16 tokens in the group
+  }
+}
+
+template <int F, int P, int D, int NC>
+__global__ __launch_bounds__(256, 2) void moe_down_wide(const _Float16* __restrict__ hi, const _Float16* __restrict__ lo,
+                                                     const int* __restrict__ ids_g, const u32x4* __restrict__ wp,
+                                                     const _Float16* __restrict__ scales, float* __restrict__ part,
+                                                     MoeShape s, int by_pair) {
+  static_assert(D % 2 == 0, "two column buffers");
+  __shared__ short col_pair[4][kGroup];
+  __shared__ half8v bufh0[512 * NC], bufh1[512 * NC], bufl0[512 * NC], bufl1[512 * NC];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int t0 = blockIdx.z * kGroup;
+  const int tokens = s.T - t0 < kGroup ? s.T - t0 : kGroup;
+  const int* ids = ids_g + static_cast<int64_t>(t0) * s.k;
+  const int slot = blockIdx.y;
+  int e = slot;
+  if (by_pair) {
+    if (slot >= tokens * s.k) return;
+    e = __builtin_amdgcn_readfirstlane(ids[slot]);
+    if (e < 0 || e >= s.E) return;
+  }
+  const Choice ch = choice_of<false>(ids, nullptr, tokens, s.k, e, lane);
+  const int ktiles = s.I >> 8;
+  const int nb = (blockIdx.x * 4 + wave) * P;
+  const int64_t kstr = static_cast<int64_t>(s.H >> 4) * Fmt<F>::kTileQuads;
+  const u32x4* w = wp + static_cast<int64_t>(e) * ktiles * kstr + nb * static_cast<int64_t>(Fmt<F>::kTileQuads) + lane;
+  _Float16 sw[P];
+  const _Float16* sc = scales + static_cast<int64_t>(e) * s.H + nb * 16 + r;
+#pragma unroll
+  for (int p = 0; p < P; ++p) sw[p] = sc[16 * p];
+  const uint64_t mask = __ballot(ch.first >= 0);
+  if (!has_work(mask, ch.first, by_pair, slot)) return;
+  const int n = __popcll(mask);
+  if (ch.first >= 0) col_pair[wave][__popcll(mask & ((uint64_t(1) << lane) - 1))] = static_cast<short>(ch.first);
+  __builtin_amdgcn_wave_barrier();
+  typename Fmt<F>::Tile tw[D][P];
+  constexpr int kW = P * Fmt<F>::kTileLoads;
+  auto load_w = [&](int slot_, int kt) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) Fmt<F>::template load<true>(tw[slot_][p], w + kt * kstr + p * Fmt<F>::kTileQuads, lane);
+  };
+  auto pass = [&](int c0, auto C) {
+    constexpr int nc = decltype(C)::value;
+    const _Float16 *srch[nc][2], *srcl[nc][2];
+#pragma unroll
+    for (int q = 0; q < nc; ++q)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = 4 * wave + 2 * i + (lane >> 5), c = c0 + 16 * q + col;
+        const int64_t at = (static_cast<int64_t>(t0) * s.k + col_pair[wave][c < n ? c : c0]) * s.I + 8 * ((lane & 31) ^ (col & 7));
+        srch[q][i] = hi + at;
+        srcl[q][i] = lo + at;
+      }
+    auto columns = [&](half8v* bh, half8v* bl, int kt) {
+#pragma unroll
+      for (int q = 0; q < nc; ++q) {
+        load_columns(bh + 512 * q, srch[q], kt, wave);
+        load_columns(bl + 512 * q, srcl[q], kt, wave);
+      }
+    };
+    columns(bufh0, bufl0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int d = 0; d < D; ++d) load_w(d, d < ktiles ? d : 0);
+    float4v ah[nc][P], al[nc][P];
+#pragma unroll
+    for (int q = 0; q < nc; ++q)
+#pragma unroll
+      for (int p = 0; p < P; ++p) ah[q][p] = al[q][p] = float4v{0.f, 0.f, 0.f, 0.f};
+    auto tile = [&](int kt, auto U) {
+      constexpr int u = decltype(U)::value;
+      const half8v *curh = u & 1 ? bufh1 : bufh0, *curl = u & 1 ? bufl1 : bufl0;
+      __builtin_amdgcn_sched_barrier(0);
+      if (kt == 0) wait_vm<D * kW>();
+      else if (kt - 1 + D < ktiles) wait_vm<kW>();
+      else wait_vm<0>();
+      barrier_no_fence();
+      if (kt + 1 < ktiles) {
+        if (u & 1) columns(bufh0, bufl0, kt + 1);
+        else columns(bufh1, bufl1, kt + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      half2v s2[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) s2[p] = scale2_of<F>(sw[p]);
+      auto step = [&](auto J) {
+        constexpr int j = decltype(J)::value;
+        const int at = r * 32 + ((4 * j + g) ^ (r & 7));
+        half8v xh[nc], xl[nc];
+#pragma unroll
+        for (int q = 0; q < nc; ++q) {
+          xh[q] = curh[512 * q + at];
+          xl[q] = curl[512 * q + at];
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const half8v a = Fmt<F>::template step<j>(tw[u][p], s2[p]);
+#pragma unroll
+          for (int q = 0; q < nc; ++q) {
+            ah[q][p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, xh[q], ah[q][p], 0, 0, 0);
+            al[q][p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, xl[q], al[q][p], 0, 0, 0);
+          }
+        }
+      };
+      step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
+      step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
+      step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
+      step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
+      __builtin_amdgcn_sched_barrier(0);
+      if (kt + D < ktiles) load_w(u, kt + D);
+    };
+    for (int kt = 0; kt < ktiles; kt += D) {
+      tile(kt, std::integral_constant<int, 0>{});
+      if (kt + 1 < ktiles) tile(kt + 1, std::integral_constant<int, 1>{});
+      if constexpr (D > 2) {
+        if (kt + 2 < ktiles) tile(kt + 2, std::integral_constant<int, 2>{});
+        if (kt + 3 < ktiles) tile(kt + 3, std::integral_constant<int, 3>{});
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < nc; ++q) {
+      const int c = c0 + 16 * q + r;
+      if (c < n) {
+        float* dst = part + (static_cast<int64_t>(t0) * s.k + col_pair[wave][c]) * s.H + nb * 16 + 4 * g;
+#pragma unroll
+        for (int p = 0; p < P; ++p) *reinterpret_cast<float4v*>(dst + 16 * p) = ah[q][p] + al[q][p] * (1.0f / kLoScale);
+      }
+    }
+  };
+  if constexpr (NC == 2) {
+    int c0 = 0;
+    for (; n - c0 > 16; c0 += 32) {
+      pass(c0, std::integral_constant<int, 2>{});
+      __syncthreads();
+    }
+    if (c0 < n) pass(c0, std::integral_constant<int, 1>{});
+  } else {
+    pass(0, std::integral_constant<int, 1>{});
+  }
+}
+
+// 4 rows of a token per thread.
 __global__ __launch_bounds__(256) void moe_sum(const float* __restrict__ part, const int* __restrict__ ids,
                                                _Float16* __restrict__ Y, MoeShape s) {
   const int64_t t = blockIdx.y;
   const int row = 4 * (blockIdx.x * 256 + threadIdx.x);
   if (row >= s.H) return;
+  ids += t * s.k;
   const float* p = part + t * s.k * s.H + row;
-  sum_choices(ids + t * s.k, s, [&](int j) { return *reinterpret_cast<const float4v*>(p + static_cast<int64_t>(j) * s.H); },
-              Y + t * s.H + row);
+  float4v v[kMaxK];
+  int id[kMaxK];
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) id[j] = j < s.k ? ids[j] : -1;
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    bool use = id[j] >= 0 && id[j] < s.E;
+#pragma unroll
+    for (int o = 0; o < j; ++o) use = use && id[o] != id[j];  // the same expert again: counted with the first
+    v[j] = float4v{0.f, 0.f, 0.f, 0.f};
+    if (use) v[j] = *reinterpret_cast<const float4v*>(p + static_cast<int64_t>(j) * s.H);
+  }
+  float4v sum = v[0];
+#pragma unroll
+  for (int j = 1; j < kMaxK; ++j)
+    if (j < s.k) sum += v[j];
+  half4v o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = static_cast<_Float16>(sum[i] * (1.0f / kHScale));
+  *reinterpret_cast<half4v*>(Y + t * s.H + row) = o;
+}
+
+// ---------------------------------------------------------------------------
+// Down product and the sum over experts, few tokens (at most kFewPairs pairs and
+// kFewTiles tiles of each row block):
+// a workgroup of 16 waves owns 16 rows of the output.  The columns of the MFMAs
+// are the tokens themselves, with zeros where a token did not choose the tile's
+// expert, so an output is one long product over (expert, k) and nothing but the
+// waves' sums has to be added: no parts in memory, no second kernel.  The waves
+// share the list of (expert, k-tile) of the experts that any token chose, in
+// the order of first choice, in equal contiguous parts, and add in wave order.
+// ---------------------------------------------------------------------------
+template <int F>
+__global__ __launch_bounds__(1024) void moe_down_few(const _Float16* __restrict__ hi, const _Float16* __restrict__ lo,
+                                                     const int* __restrict__ ids, const u32x4* __restrict__ wp,
+                                                     const _Float16* __restrict__ scales, _Float16* __restrict__ Y,
+                                                     MoeShape s) {
+  constexpr int kWaves = 16;
+  __shared__ short s_ids[kFewPairs];
+  __shared__ short s_active[kFewPairs];
+  __shared__ float4v red[kWaves][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int pairs = s.T * s.k, ktiles = s.I >> 8, nb = blockIdx.x;
+  // Every wave makes the list for itself: lane = pair; a pair whose expert no
+  // earlier pair chose stands for the expert.
+  int id = lane < pairs ? ids[lane] : -1;
+  if (id >= s.E) id = -1;
+  if (wave == 0) s_ids[lane] = static_cast<short>(id < 0 ? -1 : id);
+  bool first = id >= 0;
+  for (int o = 0; o + 1 < pairs; ++o) {
+    const int other = __builtin_amdgcn_readlane(id, o);
+    first = first && (o >= lane || other != id);
+  }
+  const uint64_t mask = __ballot(first);
+  const int na = __popcll(mask);
+  if (wave == 0 && first) s_active[__popcll(mask & ((uint64_t(1) << lane) - 1))] = static_cast<short>(id);
+  __syncthreads();
+  const int total = na * ktiles;
+  const int f0 = wave * total / kWaves, f1 = (wave + 1) * total / kWaves;
+  const int64_t kstr = static_cast<int64_t>(s.H >> 4) * Fmt<F>::kTileQuads;
+  const u32x4* w0 = wp + nb * static_cast<int64_t>(Fmt<F>::kTileQuads) + lane;
+  float4v ah = {0.f, 0.f, 0.f, 0.f}, al = {0.f, 0.f, 0.f, 0.f};
+  struct Weights {
+    typename Fmt<F>::Tile t;
+    _Float16 scale;
+  };
+  struct Values {
+    half8v h[8], l[8];
+  };
+  auto expert_of = [&](int f) { return __builtin_amdgcn_readfirstlane(s_active[f / ktiles]); };
+  auto load_w = [&](Weights& w, int f) {
+    const int e = expert_of(f), kt = f % ktiles;
+    Fmt<F>::template load<true>(w.t, w0 + (static_cast<int64_t>(e) * ktiles + kt) * kstr, lane);
+    w.scale = scales[static_cast<int64_t>(e) * s.H + nb * 16 + r];
+  };
+  auto load_h = [&](Values& v, int f) {
+    const int e = expert_of(f), kt = f % ktiles;
+    // Column r is token r (behind the last: the last, not stored); its pair of this expert, if any.
+    const int t = r < s.T ? r : s.T - 1;
+    int pair = -1;
+    for (int j = s.k - 1; j >= 0; --j)
+      if (s_ids[t * s.k + j] == e) pair = t * s.k + j;
+    const bool mine = pair >= 0;
+    const int64_t at = static_cast<int64_t>(mine ? pair : 0) * s.I + kt * 256 + 8 * g;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v.h[j] = v.l[j] = half8v{};
+      if (mine) {
+        v.h[j] = *reinterpret_cast<const half8v*>(hi + at + 32 * j);
+        v.l[j] = *reinterpret_cast<const half8v*>(lo + at + 32 * j);
+      }
+    }
+  };
+  auto mul = [&](const Weights& w, const Values& v) {
+    const half2v s2 = scale2_of<F>(w.scale);
+    auto step = [&](auto J) {
+      constexpr int j = decltype(J)::value;
+      const half8v a = Fmt<F>::template step<j>(w.t, s2);
+      ah = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, v.h[j], ah, 0, 0, 0);
+      al = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, v.l[j], al, 0, 0, 0);
+    };
+    step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
+    step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
+    step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
+  };
+  // At most two tiles per wave: the second's weights are requested before the first is multiplied.
+  if (f0 < f1) {
+    Weights wa, wb;
+    Values v;
+    load_w(wa, f0);
+    load_h(v, f0);
+    load_w(wb, f1 - 1);
+    __builtin_amdgcn_sched_barrier(0);
+    mul(wa, v);
+    if (f0 + 1 < f1) {
+      load_h(v, f0 + 1);
+      mul(wb, v);
+    }
+  }
+  red[wave][lane] = ah + al * (1.0f / kLoScale);
+  __syncthreads();
+  if (wave == 0 && r < s.T) {
+    const float4v sum = reduce_waves<kWaves>(red, lane);
+    half4v o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = static_cast<_Float16>(sum[i] * (1.0f / kHScale));
+    *reinterpret_cast<half4v*>(Y + static_cast<int64_t>(r) * s.H + nb * 16 + 4 * g) = o;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -556,7 +983,7 @@ bool moe_sizes_ok(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Workspace {
-  size_t logits, hi, lo, part, counters, bytes;
+  size_t logits, hi, lo, part, bytes;
 };
 Workspace workspace_of(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
   Workspace w;
@@ -565,8 +992,7 @@ Workspace workspace_of(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
   w.hi = round256(static_cast<size_t>(T) * E * sizeof(double));
   w.lo = w.hi + round256(pairs * I * 2);
   w.part = w.lo + round256(pairs * I * 2);
-  w.counters = w.part + round256(pairs * H * sizeof(float));
-  w.bytes = w.counters + row_groups(H) * sizeof(unsigned);
+  w.bytes = w.part + round256(pairs * H * sizeof(float));
   return w;
 }
 
@@ -578,7 +1004,6 @@ struct MoeCall {
   const _Float16 *gate_up_scales, *down_scales;
   _Float16 *Y, *hi, *lo;
   float* part;
-  unsigned* counters;
   MoeShape s;
   hipStream_t stream;
 };
@@ -614,7 +1039,8 @@ int launch_experts(const MoeCall& c, const double* logits, int renorm) {
   const unsigned groups = static_cast<unsigned>(fpx_ceil_div(s.T, kGroup));
   int by_pair = group_tokens * s.k < s.E;
   int slots = by_pair ? group_tokens * s.k : s.E;
-  const unsigned grid_y = static_cast<unsigned>(slots) * static_cast<unsigned>(fpx_ceil_div(group_tokens, 16));
+  const unsigned grid_y = static_cast<unsigned>(slots);
+  const bool two = group_tokens > 16;  // two groups of 16 columns at once
   const int cus = fpx::current_cus();
   const _Float16* X = c.X;
   int* ids = c.ids;
@@ -622,11 +1048,22 @@ int launch_experts(const MoeCall& c, const double* logits, int renorm) {
   const u32x4* w = c.gate_up;
   const _Float16* sc = c.gate_up_scales;
   _Float16 *hi = c.hi, *lo = c.lo, *Y = c.Y;
-  unsigned* counters = c.counters;
   float* part = c.part;
-  {
+  // The forms that share the token fragments, where they give every CU two workgroups.
+  const int64_t wide_gu = static_cast<int64_t>(slots) * (s.I / 16), wide_dn = static_cast<int64_t>(slots) * (s.H / 16);
+  if (!logits && wide_gu >= 8 * cus) {
+    const int p = wide_gu >= 16 * cus ? 2 : 1;
+    void* args[] = {&X, &ids, &weights, &w, &sc, &hi, &lo, &s, &by_pair};
+    const dim3 grid(static_cast<unsigned>(s.I / 16 / (4 * p)), grid_y, groups);
+    const void* kern = p == 2 ? (two ? reinterpret_cast<const void*>(&moe_gate_up_wide<F, 2, 2, 2>)
+                                     : reinterpret_cast<const void*>(&moe_gate_up_wide<F, 2, 2, 1>))
+                              : (two ? reinterpret_cast<const void*>(&moe_gate_up_wide<F, 1, 4, 2>)
+                                     : reinterpret_cast<const void*>(&moe_gate_up_wide<F, 1, 4, 1>));
+    const int st = moe_launch(kern, grid, dim3(256), args, c.stream);
+    if (st != FP6_OK) return st;
+  } else {
     Split sp = choose_split(s.I / 16, s.H / 256, slots, cus);
-    void* args[] = {&X, &logits, &ids, &weights, &w, &sc, &hi, &lo, &counters, &s, &sp.ks, &by_pair, &slots, &renorm};
+    void* args[] = {&X, &logits, &ids, &weights, &w, &sc, &hi, &lo, &s, &sp.ks, &by_pair, &renorm};
     const dim3 grid(static_cast<unsigned>(s.I / 16 / (4 / sp.ks * sp.p)), grid_y, groups);
     const void* kern = nullptr;
     if (logits)
@@ -642,21 +1079,32 @@ int launch_experts(const MoeCall& c, const double* logits, int renorm) {
   }
   w = c.down;
   sc = c.down_scales;
-  Split sp = choose_split(s.H / 16, s.I / 256, slots, cus);
-  void* args[] = {&hi, &lo, &ids, &w, &sc, &part, &counters, &Y, &s, &sp.ks, &by_pair, &slots};
-  const dim3 grid(static_cast<unsigned>(s.H / 16 / (4 / sp.ks * sp.p)), grid_y, groups);
-  const bool sum = s.T <= kFusedT;
-  const void* kern = nullptr;
-  if (sum)
-    kern = sp.p == 4   ? reinterpret_cast<const void*>(&moe_down<F, 4, 1, true>)
-           : sp.p == 2 ? reinterpret_cast<const void*>(&moe_down<F, 2, 1, true>)
-                       : reinterpret_cast<const void*>(&moe_down<F, 1, 2, true>);
-  else
-    kern = sp.p == 4   ? reinterpret_cast<const void*>(&moe_down<F, 4, 1, false>)
-           : sp.p == 2 ? reinterpret_cast<const void*>(&moe_down<F, 2, 1, false>)
-                       : reinterpret_cast<const void*>(&moe_down<F, 1, 2, false>);
-  const int st = moe_launch(kern, grid, dim3(256), args, c.stream);
-  if (st != FP6_OK || sum) return st;
+  // The waves of moe_down_few go through their tiles one after another: up to
+  // two each (16 waves), and one lane per pair.
+  if (s.T <= 16 && s.T * s.k <= kFewPairs && s.T * s.k * (s.I / 256) <= kFewTiles) {
+    void* args[] = {&hi, &lo, &ids, &w, &sc, &Y, &s};
+    return moe_launch(reinterpret_cast<const void*>(&moe_down_few<F>), dim3(static_cast<unsigned>(s.H / 16)), dim3(1024),
+                      args, c.stream);
+  }
+  int st = FP6_OK;
+  if (wide_dn >= 16 * cus) {
+    const int p = !two && wide_dn >= 32 * cus ? 4 : 2;  // two column groups: no registers for four row blocks
+    void* args[] = {&hi, &lo, &ids, &w, &sc, &part, &s, &by_pair};
+    const dim3 grid(static_cast<unsigned>(s.H / 16 / (4 * p)), grid_y, groups);
+    const void* kern = p == 4 ? reinterpret_cast<const void*>(&moe_down_wide<F, 4, 2, 1>)
+                              : (two ? reinterpret_cast<const void*>(&moe_down_wide<F, 2, 4, 2>)
+                                     : reinterpret_cast<const void*>(&moe_down_wide<F, 2, 4, 1>));
+    st = moe_launch(kern, grid, dim3(256), args, c.stream);
+  } else {
+    Split sp = choose_split(s.H / 16, s.I / 256, slots, cus);
+    void* args[] = {&hi, &lo, &ids, &w, &sc, &part, &s, &sp.ks, &by_pair};
+    const dim3 grid(static_cast<unsigned>(s.H / 16 / (4 / sp.ks * sp.p)), grid_y, groups);
+    const void* kern = sp.p == 4   ? reinterpret_cast<const void*>(&moe_down<F, 4, 1>)
+                       : sp.p == 2 ? reinterpret_cast<const void*>(&moe_down<F, 2, 1>)
+                                   : reinterpret_cast<const void*>(&moe_down<F, 1, 2>);
+    st = moe_launch(kern, grid, dim3(256), args, c.stream);
+  }
+  if (st != FP6_OK) return st;
   void* sum_args[] = {&part, &ids, &Y, &s};
   // The grid's second dimension takes T <= 65536 tokens in two parts.
   for (int t = 0; t < s.T; t += 32768) {
@@ -725,7 +1173,6 @@ MoeCall make_call(const void* X, const void* ids, const void* weights, const voi
   c.hi = reinterpret_cast<_Float16*>(ws + w.hi);
   c.lo = reinterpret_cast<_Float16*>(ws + w.lo);
   c.part = reinterpret_cast<float*>(ws + w.part);
-  c.counters = reinterpret_cast<unsigned*>(ws + w.counters);
   c.s = MoeShape{static_cast<int>(T), static_cast<int>(E), static_cast<int>(k), static_cast<int>(H), static_cast<int>(I)};
   c.stream = static_cast<hipStream_t>(stream);
   return c;
