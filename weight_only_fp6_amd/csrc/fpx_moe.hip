@@ -188,6 +188,19 @@ __device__ __forceinline__ Choice choice_of(const int* __restrict__ ids, const f
   return c;
 }
 
+// The same where there is one token only: lane = choice, wave-uniform result.
+__device__ __forceinline__ Choice choice_of_one(const int* __restrict__ ids, const float* __restrict__ weights, int k,
+                                                int e, int lane) {
+  const int id = lane < k ? ids[lane] : -1;
+  const float w = lane < k ? weights[lane] : 0.0f;
+  uint64_t hits = __ballot(lane < k && id == e);
+  Choice c{hits ? __ffsll(static_cast<unsigned long long>(hits)) - 1 : -1, 0.0f};
+  for (; hits; hits &= hits - 1)
+    c.weight += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w),
+                                                                    __ffsll(static_cast<unsigned long long>(hits)) - 1));
+  return c;
+}
+
 // Whether this workgroup has work: any token chose its expert, and (slots by
 // pair) the slot's pair is the expert's first.
 __device__ __forceinline__ bool has_work(uint64_t mask, int first, int by_pair, int slot) {
@@ -235,6 +248,15 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up(const _Float16* __restrict
   const bool first_wg = blockIdx.x == 0 && blockIdx.y == 0;
   const int* ids = ids_g + static_cast<int64_t>(t0) * s.k;
   const float* weights = weights_g + static_cast<int64_t>(t0) * s.k;
+  const int kslice = wave % ks, ktiles = s.H >> 8;
+  const int kt0 = kslice * ktiles / ks, kt1 = (kslice + 1) * ktiles / ks;  // never empty: ks <= ktiles
+  // One token: every column repeats it, and it is known before its experts are.
+  const bool one = s.T == 1;
+  half8v xf[2][8];
+  if (one) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) xf[0][j] = *reinterpret_cast<const half8v*>(X + 8 * g + kt0 * 256 + 32 * j);
+  }
   if constexpr (FUSED) {
     if (wave < tokens) {
       int id;
@@ -260,15 +282,14 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up(const _Float16* __restrict
     e = __builtin_amdgcn_readfirstlane(ids[slot]);
     if (e < 0 || e >= s.E) return;
   }
-  const Choice ch = choice_of<true>(ids, weights, tokens, s.k, e, lane);
+  const Choice ch = one ? choice_of_one(ids, weights, s.k, e, lane) : choice_of<true>(ids, weights, tokens, s.k, e, lane);
 
-  const int rb = wave / ks, kslice = wave - rb * ks;
-  const int iblocks = s.I >> 4, ktiles = s.H >> 8;
+  const int rb = wave / ks;
+  const int iblocks = s.I >> 4;
   const int nb = (blockIdx.x * (4 / ks) + rb) * P;
   const int64_t kstr = 2 * static_cast<int64_t>(iblocks) * Fmt<F>::kTileQuads;
   const u32x4* wg = wp + static_cast<int64_t>(e) * ktiles * kstr + nb * static_cast<int64_t>(Fmt<F>::kTileQuads) + lane;
   const u32x4* wu = wg + static_cast<int64_t>(iblocks) * Fmt<F>::kTileQuads;
-  const int kt0 = kslice * ktiles / ks, kt1 = (kslice + 1) * ktiles / ks;  // never empty: ks <= ktiles
   typename Fmt<F>::Tile tg[D][P], tu[D][P];
   _Float16 sg[P], su[P];
   const _Float16* sc = scales + static_cast<int64_t>(e) * 2 * s.I + nb * 16 + r;
@@ -289,10 +310,10 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up(const _Float16* __restrict
     sg[p] = sc[16 * p];
     su[p] = sc[s.I + 16 * p];
   }
-  const uint64_t mask = __ballot(ch.first >= 0);
+  const uint64_t mask = one ? uint64_t(ch.first >= 0) : __ballot(ch.first >= 0);
   if (!has_work(mask, ch.first, by_pair, slot)) return;
   const int n = __popcll(mask);
-  if (ch.first >= 0) {
+  if (ch.first >= 0 && !one) {
     const int c = __popcll(mask & ((uint64_t(1) << lane) - 1));
     col_token[wave][c] = static_cast<short>(lane);
     col_pair[wave][c] = static_cast<short>(ch.first);
@@ -300,72 +321,73 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up(const _Float16* __restrict
   }
   __builtin_amdgcn_wave_barrier();
   for (int c0 = 0; c0 < n; c0 += 16) {
-  if (c0 > 0) {
-    __syncthreads();
-    load_first();
-  }
-  // Column r; columns behind the expert's last token repeat the first of the 16 and are not stored.
-  const int c = c0 + r < n ? c0 + r : c0;
-  const _Float16* xr = X + static_cast<int64_t>(t0 + col_token[wave][c]) * s.H + 8 * g;
-  half8v xf[2][8];
+    if (c0 > 0) {
+      __syncthreads();
+      load_first();
+    }
+    // Column r; columns behind the expert's last token repeat the first of the 16 and are not stored.
+    const int c = c0 + r < n ? c0 + r : c0;
+    const _Float16* xr = X + static_cast<int64_t>(t0 + (one ? 0 : col_token[wave][c])) * s.H + 8 * g;
+    if (!one) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) xf[0][j] = *reinterpret_cast<const half8v*>(xr + kt0 * 256 + 32 * j);
-  float4v ag[P], au[P];
+      for (int j = 0; j < 8; ++j) xf[0][j] = *reinterpret_cast<const half8v*>(xr + kt0 * 256 + 32 * j);
+    }
+    float4v ag[P], au[P];
 #pragma unroll
-  for (int p = 0; p < P; ++p) ag[p] = au[p] = float4v{0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < P; ++p) ag[p] = au[p] = float4v{0.f, 0.f, 0.f, 0.f};
 
-  auto tile = [&](int kt, auto CUR) {
-    constexpr int cur = decltype(CUR)::value;
-    const int next = kt + 1 < kt1 ? kt + 1 : kt;  // behind the end: a stand-in
+    auto tile = [&](int kt, auto CUR) {
+      constexpr int cur = decltype(CUR)::value;
+      const int next = kt + 1 < kt1 ? kt + 1 : kt;  // behind the end: a stand-in
 #pragma unroll
-    for (int j = 0; j < 8; ++j) xf[1 - cur][j] = *reinterpret_cast<const half8v*>(xr + next * 256 + 32 * j);
-    __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < 8; ++j) xf[1 - cur][j] = *reinterpret_cast<const half8v*>(xr + next * 256 + 32 * j);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const half2v s2g = scale2_of<F>(sg[p]), s2u = scale2_of<F>(su[p]);
+        auto step = [&](auto J) {
+          constexpr int j = decltype(J)::value;
+          ag[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(Fmt<F>::template step<j>(tg[cur % D][p], s2g), xf[cur][j], ag[p], 0, 0, 0);
+          au[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(Fmt<F>::template step<j>(tu[cur % D][p], s2u), xf[cur][j], au[p], 0, 0, 0);
+        };
+        step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
+        step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
+        step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
+        step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
+        __builtin_amdgcn_sched_barrier(0);
+        if (kt + D < kt1) {
+          Fmt<F>::template load<true>(tg[cur % D][p], wg + (kt + D) * kstr + p * Fmt<F>::kTileQuads, lane);
+          Fmt<F>::template load<true>(tu[cur % D][p], wu + (kt + D) * kstr + p * Fmt<F>::kTileQuads, lane);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    int kt = kt0;
+    for (; kt + 2 <= kt1; kt += 2) {
+      tile(kt, std::integral_constant<int, 0>{});
+      tile(kt + 1, std::integral_constant<int, 1>{});
+    }
+    if (kt < kt1) tile(kt, std::integral_constant<int, 0>{});
+
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const half2v s2g = scale2_of<F>(sg[p]), s2u = scale2_of<F>(su[p]);
-      auto step = [&](auto J) {
-        constexpr int j = decltype(J)::value;
-        ag[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(Fmt<F>::template step<j>(tg[cur % D][p], s2g), xf[cur][j], ag[p], 0, 0, 0);
-        au[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(Fmt<F>::template step<j>(tu[cur % D][p], s2u), xf[cur][j], au[p], 0, 0, 0);
-      };
-      step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
-      step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
-      step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
-      step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
-      __builtin_amdgcn_sched_barrier(0);
-      if (kt + D < kt1) {
-        Fmt<F>::template load<true>(tg[cur % D][p], wg + (kt + D) * kstr + p * Fmt<F>::kTileQuads, lane);
-        Fmt<F>::template load<true>(tu[cur % D][p], wu + (kt + D) * kstr + p * Fmt<F>::kTileQuads, lane);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+      red[wave][2 * p][lane] = ag[p];
+      red[wave][2 * p + 1][lane] = au[p];
     }
-  };
-  int kt = kt0;
-  for (; kt + 2 <= kt1; kt += 2) {
-    tile(kt, std::integral_constant<int, 0>{});
-    tile(kt + 1, std::integral_constant<int, 1>{});
-  }
-  if (kt < kt1) tile(kt, std::integral_constant<int, 0>{});
-
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    red[wave][2 * p][lane] = ag[p];
-    red[wave][2 * p + 1][lane] = au[p];
-  }
-  __syncthreads();
-  // Wave (rb, kslice) sums and stores the row blocks kslice, kslice + ks, ...
-  if (c0 + r < n) {
-    const int64_t at = (static_cast<int64_t>(t0) * s.k + col_pair[wave][c]) * s.I + nb * 16 + 4 * g;
-    const float w = col_w[wave][c];
-    for (int p = kslice; p < P; p += ks) {
-      float4v vg = red[rb * ks][2 * p][lane], vu = red[rb * ks][2 * p + 1][lane];
-      for (int q = 1; q < ks; ++q) {
-        vg += red[rb * ks + q][2 * p][lane];
-        vu += red[rb * ks + q][2 * p + 1][lane];
+    __syncthreads();
+    // Wave (rb, kslice) sums and stores the row blocks kslice, kslice + ks, ...
+    if (c0 + r < n) {
+      const int64_t at = (static_cast<int64_t>(t0) * s.k + (one ? ch.first : col_pair[wave][c])) * s.I + nb * 16 + 4 * g;
+      const float w = one ? ch.weight : col_w[wave][c];
+      for (int p = kslice; p < P; p += ks) {
+        float4v vg = red[rb * ks][2 * p][lane], vu = red[rb * ks][2 * p + 1][lane];
+        for (int q = 1; q < ks; ++q) {
+          vg += red[rb * ks + q][2 * p][lane];
+          vu += red[rb * ks + q][2 * p + 1][lane];
+        }
+        store_gated(hi + at + 16 * p, lo + at + 16 * p, vg, vu, w);
       }
-      store_gated(hi + at + 16 * p, lo + at + 16 * p, vg, vu, w);
     }
-  }
   }
 }
 
@@ -449,68 +471,68 @@ __global__ __launch_bounds__(256, 2) void moe_down(const _Float16* __restrict__ 
   if (ch.first >= 0) col_pair[wave][__popcll(mask & ((uint64_t(1) << lane) - 1))] = static_cast<short>(ch.first);
   __builtin_amdgcn_wave_barrier();
   for (int c0 = 0; c0 < n; c0 += 16) {
-  if (c0 > 0) {
-    __syncthreads();
-    load_first();
-  }
-  const int c = c0 + r < n ? c0 + r : c0;
-  const int pair = col_pair[wave][c];
-  const int64_t at = (static_cast<int64_t>(t0) * s.k + pair) * s.I + 8 * g;
-  const _Float16 *hr = hi + at, *lr = lo + at;
-  half8v fh[2][8], fl[2][8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    fh[0][j] = *reinterpret_cast<const half8v*>(hr + kt0 * 256 + 32 * j);
-    fl[0][j] = *reinterpret_cast<const half8v*>(lr + kt0 * 256 + 32 * j);
-  }
-  float4v ah[P], al[P];
-#pragma unroll
-  for (int p = 0; p < P; ++p) ah[p] = al[p] = float4v{0.f, 0.f, 0.f, 0.f};
-  auto tile = [&](int kt, auto CUR) {
-    constexpr int cur = decltype(CUR)::value;
-    const int next = kt + 1 < kt1 ? kt + 1 : kt;  // behind the end: a stand-in
+    if (c0 > 0) {
+      __syncthreads();
+      load_first();
+    }
+    const int c = c0 + r < n ? c0 + r : c0;
+    const int pair = col_pair[wave][c];
+    const int64_t at = (static_cast<int64_t>(t0) * s.k + pair) * s.I + 8 * g;
+    const _Float16 *hr = hi + at, *lr = lo + at;
+    half8v fh[2][8], fl[2][8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      fh[1 - cur][j] = *reinterpret_cast<const half8v*>(hr + next * 256 + 32 * j);
-      fl[1 - cur][j] = *reinterpret_cast<const half8v*>(lr + next * 256 + 32 * j);
+      fh[0][j] = *reinterpret_cast<const half8v*>(hr + kt0 * 256 + 32 * j);
+      fl[0][j] = *reinterpret_cast<const half8v*>(lr + kt0 * 256 + 32 * j);
     }
-    __builtin_amdgcn_sched_barrier(0);
+    float4v ah[P], al[P];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const half2v s2 = scale2_of<F>(sw[p]);
-      auto step = [&](auto J) {
-        constexpr int j = decltype(J)::value;
-        const half8v a = Fmt<F>::template step<j>(tw[cur % D][p], s2);
-        ah[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fh[cur][j], ah[p], 0, 0, 0);
-        al[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fl[cur][j], al[p], 0, 0, 0);
-      };
-      step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
-      step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
-      step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
-      step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
-      __builtin_amdgcn_sched_barrier(0);
-      if (kt + D < kt1)
-        Fmt<F>::template load<true>(tw[cur % D][p], w + (kt + D) * kstr + p * Fmt<F>::kTileQuads, lane);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  int kt = kt0;
-  for (; kt + 2 <= kt1; kt += 2) {
-    tile(kt, std::integral_constant<int, 0>{});
-    tile(kt + 1, std::integral_constant<int, 1>{});
-  }
-  if (kt < kt1) tile(kt, std::integral_constant<int, 0>{});
+    for (int p = 0; p < P; ++p) ah[p] = al[p] = float4v{0.f, 0.f, 0.f, 0.f};
+    auto tile = [&](int kt, auto CUR) {
+      constexpr int cur = decltype(CUR)::value;
+      const int next = kt + 1 < kt1 ? kt + 1 : kt;  // behind the end: a stand-in
 #pragma unroll
-  for (int p = 0; p < P; ++p) red[wave][p][lane] = ah[p] + al[p] * (1.0f / kLoScale);
-  __syncthreads();
-  if (c0 + r < n) {
-    const int64_t dst = static_cast<int64_t>(pair) * s.H + rows0 + rb * P * 16 + 4 * g;
-    for (int p = kslice; p < P; p += ks) {
-      float4v v = red[rb * ks][p][lane];
-      for (int q = 1; q < ks; ++q) v += red[rb * ks + q][p][lane];
-      *reinterpret_cast<float4v*>(parts + dst + 16 * p) = v;
+      for (int j = 0; j < 8; ++j) {
+        fh[1 - cur][j] = *reinterpret_cast<const half8v*>(hr + next * 256 + 32 * j);
+        fl[1 - cur][j] = *reinterpret_cast<const half8v*>(lr + next * 256 + 32 * j);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const half2v s2 = scale2_of<F>(sw[p]);
+        auto step = [&](auto J) {
+          constexpr int j = decltype(J)::value;
+          const half8v a = Fmt<F>::template step<j>(tw[cur % D][p], s2);
+          ah[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fh[cur][j], ah[p], 0, 0, 0);
+          al[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fl[cur][j], al[p], 0, 0, 0);
+        };
+        step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
+        step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
+        step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
+        step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
+        __builtin_amdgcn_sched_barrier(0);
+        if (kt + D < kt1)
+          Fmt<F>::template load<true>(tw[cur % D][p], w + (kt + D) * kstr + p * Fmt<F>::kTileQuads, lane);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    int kt = kt0;
+    for (; kt + 2 <= kt1; kt += 2) {
+      tile(kt, std::integral_constant<int, 0>{});
+      tile(kt + 1, std::integral_constant<int, 1>{});
     }
-  }
+    if (kt < kt1) tile(kt, std::integral_constant<int, 0>{});
+#pragma unroll
+    for (int p = 0; p < P; ++p) red[wave][p][lane] = ah[p] + al[p] * (1.0f / kLoScale);
+    __syncthreads();
+    if (c0 + r < n) {
+      const int64_t dst = static_cast<int64_t>(pair) * s.H + rows0 + rb * P * 16 + 4 * g;
+      for (int p = kslice; p < P; p += ks) {
+        float4v v = red[rb * ks][p][lane];
+        for (int q = 1; q < ks; ++q) v += red[rb * ks + q][p][lane];
+        *reinterpret_cast<float4v*>(parts + dst + 16 * p) = v;
+      }
+    }
   }
 }
 
@@ -575,6 +597,20 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up_wide(const _Float16* __res
     sg[p] = sc[16 * p];
     su[p] = sc[s.I + 16 * p];
   }
+  typename Fmt<F>::Tile tg[D][P], tu[D][P];
+  constexpr int kW = 2 * P * Fmt<F>::kTileLoads;  // weight loads per k-tile
+  auto load_w = [&](int slot_, int kt) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      Fmt<F>::template load<true>(tg[slot_][p], wg + kt * kstr + p * Fmt<F>::kTileQuads, lane);
+      Fmt<F>::template load<true>(tu[slot_][p], wu + kt * kstr + p * Fmt<F>::kTileQuads, lane);
+    }
+  };
+  auto load_ring = [&]() {
+#pragma unroll
+    for (int d = 0; d < D; ++d) load_w(d, d < ktiles ? d : 0);
+  };
+  load_ring();
   const uint64_t mask = __ballot(ch.first >= 0);
   if (!has_work(mask, ch.first, by_pair, slot)) return;
   const int n = __popcll(mask);
@@ -585,15 +621,6 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up_wide(const _Float16* __res
     col_w[wave][c] = ch.weight;
   }
   __builtin_amdgcn_wave_barrier();
-  typename Fmt<F>::Tile tg[D][P], tu[D][P];
-  constexpr int kW = 2 * P * Fmt<F>::kTileLoads;  // weight loads per k-tile
-  auto load_w = [&](int slot_, int kt) {
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      Fmt<F>::template load<true>(tg[slot_][p], wg + kt * kstr + p * Fmt<F>::kTileQuads, lane);
-      Fmt<F>::template load<true>(tu[slot_][p], wu + kt * kstr + p * Fmt<F>::kTileQuads, lane);
-    }
-  };
   // One pass: C groups of 16 columns, from column c0 on.
   auto pass = [&](int c0, auto C) {
     constexpr int nc = decltype(C)::value;
@@ -611,8 +638,6 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up_wide(const _Float16* __res
     };
     columns(buf0, 0);
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int d = 0; d < D; ++d) load_w(d, d < ktiles ? d : 0);
     float4v ag[nc][P], au[nc][P];
 #pragma unroll
     for (int q = 0; q < nc; ++q)
@@ -622,10 +647,8 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up_wide(const _Float16* __res
       constexpr int u = decltype(U)::value;
       const half8v* cur = u & 1 ? buf1 : buf0;
       __builtin_amdgcn_sched_barrier(0);
-      // Behind this k-tile's columns: at first all D k-tiles of weights, later
-      // those of k-tile t-1+D, at the end nothing.
-      if (kt == 0) wait_vm<D * kW>();
-      else if (kt - 1 + D < ktiles) wait_vm<kW>();
+      // Behind this k-tile's columns: the weights of k-tile t-1+D, if any.
+      if (kt > 0 && kt - 1 + D < ktiles) wait_vm<kW>();
       else wait_vm<0>();
       barrier_no_fence();
       if (kt + 1 < ktiles) columns(u & 1 ? buf0 : buf1, kt + 1);
@@ -681,6 +704,7 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up_wide(const _Float16* __res
     for (; n - c0 > 16; c0 += 32) {
       pass(c0, std::integral_constant<int, 2>{});
       __syncthreads();  // the buffers are free again
+      if (n - c0 > 32) load_ring();
     }
     if (c0 < n) pass(c0, std::integral_constant<int, 1>{});
   } else {
@@ -717,17 +741,22 @@ __global__ __launch_bounds__(256, 2) void moe_down_wide(const _Float16* __restri
   const _Float16* sc = scales + static_cast<int64_t>(e) * s.H + nb * 16 + r;
 #pragma unroll
   for (int p = 0; p < P; ++p) sw[p] = sc[16 * p];
-  const uint64_t mask = __ballot(ch.first >= 0);
-  if (!has_work(mask, ch.first, by_pair, slot)) return;
-  const int n = __popcll(mask);
-  if (ch.first >= 0) col_pair[wave][__popcll(mask & ((uint64_t(1) << lane) - 1))] = static_cast<short>(ch.first);
-  __builtin_amdgcn_wave_barrier();
   typename Fmt<F>::Tile tw[D][P];
   constexpr int kW = P * Fmt<F>::kTileLoads;
   auto load_w = [&](int slot_, int kt) {
 #pragma unroll
     for (int p = 0; p < P; ++p) Fmt<F>::template load<true>(tw[slot_][p], w + kt * kstr + p * Fmt<F>::kTileQuads, lane);
   };
+  auto load_ring = [&]() {
+#pragma unroll
+    for (int d = 0; d < D; ++d) load_w(d, d < ktiles ? d : 0);
+  };
+  load_ring();
+  const uint64_t mask = __ballot(ch.first >= 0);
+  if (!has_work(mask, ch.first, by_pair, slot)) return;
+  const int n = __popcll(mask);
+  if (ch.first >= 0) col_pair[wave][__popcll(mask & ((uint64_t(1) << lane) - 1))] = static_cast<short>(ch.first);
+  __builtin_amdgcn_wave_barrier();
   auto pass = [&](int c0, auto C) {
     constexpr int nc = decltype(C)::value;
     const _Float16 *srch[nc][2], *srcl[nc][2];
@@ -749,8 +778,6 @@ __global__ __launch_bounds__(256, 2) void moe_down_wide(const _Float16* __restri
     };
     columns(bufh0, bufl0, 0);
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int d = 0; d < D; ++d) load_w(d, d < ktiles ? d : 0);
     float4v ah[nc][P], al[nc][P];
 #pragma unroll
     for (int q = 0; q < nc; ++q)
@@ -760,8 +787,7 @@ __global__ __launch_bounds__(256, 2) void moe_down_wide(const _Float16* __restri
       constexpr int u = decltype(U)::value;
       const half8v *curh = u & 1 ? bufh1 : bufh0, *curl = u & 1 ? bufl1 : bufl0;
       __builtin_amdgcn_sched_barrier(0);
-      if (kt == 0) wait_vm<D * kW>();
-      else if (kt - 1 + D < ktiles) wait_vm<kW>();
+      if (kt > 0 && kt - 1 + D < ktiles) wait_vm<kW>();
       else wait_vm<0>();
       barrier_no_fence();
       if (kt + 1 < ktiles) {
@@ -821,6 +847,7 @@ __global__ __launch_bounds__(256, 2) void moe_down_wide(const _Float16* __restri
     for (; n - c0 > 16; c0 += 32) {
       pass(c0, std::integral_constant<int, 2>{});
       __syncthreads();
+      if (n - c0 > 32) load_ring();
     }
     if (c0 < n) pass(c0, std::integral_constant<int, 1>{});
   } else {
@@ -880,22 +907,6 @@ __global__ __launch_bounds__(1024) void moe_down_few(const _Float16* __restrict_
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int pairs = s.T * s.k, ktiles = s.I >> 8, nb = blockIdx.x;
-  // Every wave makes the list for itself: lane = pair; a pair whose expert no
-  // earlier pair chose stands for the expert.
-  int id = lane < pairs ? ids[lane] : -1;
-  if (id >= s.E) id = -1;
-  if (wave == 0) s_ids[lane] = static_cast<short>(id < 0 ? -1 : id);
-  bool first = id >= 0;
-  for (int o = 0; o + 1 < pairs; ++o) {
-    const int other = __builtin_amdgcn_readlane(id, o);
-    first = first && (o >= lane || other != id);
-  }
-  const uint64_t mask = __ballot(first);
-  const int na = __popcll(mask);
-  if (wave == 0 && first) s_active[__popcll(mask & ((uint64_t(1) << lane) - 1))] = static_cast<short>(id);
-  __syncthreads();
-  const int total = na * ktiles;
-  const int f0 = wave * total / kWaves, f1 = (wave + 1) * total / kWaves;
   const int64_t kstr = static_cast<int64_t>(s.H >> 4) * Fmt<F>::kTileQuads;
   const u32x4* w0 = wp + nb * static_cast<int64_t>(Fmt<F>::kTileQuads) + lane;
   float4v ah = {0.f, 0.f, 0.f, 0.f}, al = {0.f, 0.f, 0.f, 0.f};
@@ -905,30 +916,6 @@ __global__ __launch_bounds__(1024) void moe_down_few(const _Float16* __restrict_
   };
   struct Values {
     half8v h[8], l[8];
-  };
-  auto expert_of = [&](int f) { return __builtin_amdgcn_readfirstlane(s_active[f / ktiles]); };
-  auto load_w = [&](Weights& w, int f) {
-    const int e = expert_of(f), kt = f % ktiles;
-    Fmt<F>::template load<true>(w.t, w0 + (static_cast<int64_t>(e) * ktiles + kt) * kstr, lane);
-    w.scale = scales[static_cast<int64_t>(e) * s.H + nb * 16 + r];
-  };
-  auto load_h = [&](Values& v, int f) {
-    const int e = expert_of(f), kt = f % ktiles;
-    // Column r is token r (behind the last: the last, not stored); its pair of this expert, if any.
-    const int t = r < s.T ? r : s.T - 1;
-    int pair = -1;
-    for (int j = s.k - 1; j >= 0; --j)
-      if (s_ids[t * s.k + j] == e) pair = t * s.k + j;
-    const bool mine = pair >= 0;
-    const int64_t at = static_cast<int64_t>(mine ? pair : 0) * s.I + kt * 256 + 8 * g;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v.h[j] = v.l[j] = half8v{};
-      if (mine) {
-        v.h[j] = *reinterpret_cast<const half8v*>(hi + at + 32 * j);
-        v.l[j] = *reinterpret_cast<const half8v*>(lo + at + 32 * j);
-      }
-    }
   };
   auto mul = [&](const Weights& w, const Values& v) {
     const half2v s2 = scale2_of<F>(w.scale);
@@ -943,18 +930,90 @@ __global__ __launch_bounds__(1024) void moe_down_few(const _Float16* __restrict_
     step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
     step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
   };
-  // At most two tiles per wave: the second's weights are requested before the first is multiplied.
-  if (f0 < f1) {
-    Weights wa, wb;
-    Values v;
-    load_w(wa, f0);
-    load_h(v, f0);
-    load_w(wb, f1 - 1);
-    __builtin_amdgcn_sched_barrier(0);
-    mul(wa, v);
-    if (f0 + 1 < f1) {
-      load_h(v, f0 + 1);
-      mul(wb, v);
+  int total = s.k * ktiles;
+  int f0 = wave * total / kWaves, f1 = (wave + 1) * total / kWaves;
+  // One token whose choices are all served and all different, as moe_layer's
+  // are: the list is the choices themselves, and a wave needs nothing but the
+  // ids of its own tiles to request everything.
+  int id = lane < pairs ? ids[lane] : -1;
+  if (id >= s.E) id = -1;
+  bool first = id >= 0;  // a pair whose expert no earlier pair chose
+  for (int o = 0; o + 1 < pairs; ++o) {
+    const int other = __builtin_amdgcn_readlane(id, o);
+    first = first && (o >= lane || other != id);
+  }
+  const uint64_t mask = __ballot(first);
+  if (s.T == 1 && __popcll(mask) == s.k) {
+    auto load_w = [&](Weights& w, int f) {
+      const int j = f / ktiles, e = __builtin_amdgcn_readlane(id, j);
+      Fmt<F>::template load<true>(w.t, w0 + (static_cast<int64_t>(e) * ktiles + (f - j * ktiles)) * kstr, lane);
+      w.scale = scales[static_cast<int64_t>(e) * s.H + nb * 16 + r];
+    };
+    auto load_h = [&](Values& v, int f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v.h[j] = *reinterpret_cast<const half8v*>(hi + static_cast<int64_t>(f) * 256 + 8 * g + 32 * j);
+        v.l[j] = *reinterpret_cast<const half8v*>(lo + static_cast<int64_t>(f) * 256 + 8 * g + 32 * j);
+      }
+    };
+    if (f0 < f1) {
+      Weights wa, wb;
+      Values v;
+      load_h(v, f0);
+      load_w(wa, f0);
+      load_w(wb, f1 - 1);
+      __builtin_amdgcn_sched_barrier(0);
+      mul(wa, v);
+      if (f0 + 1 < f1) {
+        load_h(v, f0 + 1);
+        mul(wb, v);
+      }
+    }
+  } else {
+    // The first pairs stand for their experts.
+    if (wave == 0) s_ids[lane] = static_cast<short>(id);
+    const int na = __popcll(mask);
+    if (wave == 0 && first) s_active[__popcll(mask & ((uint64_t(1) << lane) - 1))] = static_cast<short>(id);
+    __syncthreads();
+    total = na * ktiles;
+    f0 = wave * total / kWaves, f1 = (wave + 1) * total / kWaves;
+    auto expert_of = [&](int f) { return __builtin_amdgcn_readfirstlane(s_active[f / ktiles]); };
+    auto load_w = [&](Weights& w, int f) {
+      const int e = expert_of(f), kt = f % ktiles;
+      Fmt<F>::template load<true>(w.t, w0 + (static_cast<int64_t>(e) * ktiles + kt) * kstr, lane);
+      w.scale = scales[static_cast<int64_t>(e) * s.H + nb * 16 + r];
+    };
+    auto load_h = [&](Values& v, int f) {
+      const int e = expert_of(f), kt = f % ktiles;
+      // Column r is token r (behind the last: the last, not stored); its pair of this expert, if any.
+      const int t = r < s.T ? r : s.T - 1;
+      int pair = -1;
+      for (int j = s.k - 1; j >= 0; --j)
+        if (s_ids[t * s.k + j] == e) pair = t * s.k + j;
+      const bool mine = pair >= 0;
+      const int64_t at = static_cast<int64_t>(mine ? pair : 0) * s.I + kt * 256 + 8 * g;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v.h[j] = v.l[j] = half8v{};
+        if (mine) {
+          v.h[j] = *reinterpret_cast<const half8v*>(hi + at + 32 * j);
+          v.l[j] = *reinterpret_cast<const half8v*>(lo + at + 32 * j);
+        }
+      }
+    };
+    // At most two tiles per wave: the second's weights are requested before the first is multiplied.
+    if (f0 < f1) {
+      Weights wa, wb;
+      Values v;
+      load_w(wa, f0);
+      load_h(v, f0);
+      load_w(wb, f1 - 1);
+      __builtin_amdgcn_sched_barrier(0);
+      mul(wa, v);
+      if (f0 + 1 < f1) {
+        load_h(v, f0 + 1);
+        mul(wb, v);
+      }
     }
   }
   red[wave][lane] = ah + al * (1.0f / kLoScale);
@@ -1012,20 +1071,18 @@ int moe_launch(const void* kern, dim3 grid, dim3 block, void** args, hipStream_t
   return hipLaunchKernel(kern, grid, block, args, 0, stream) == hipSuccess ? FP6_OK : FP6_E_HIP;
 }
 
-// Waves that split K and row blocks per wave: the most work per workgroup
-// (fewer prologues, token fragments used for more rows) that still gives every
+// Row blocks per CU, over all slots, from which on the forms with shared
+// fragments are used (4 row blocks per workgroup at least: two workgroups).
+constexpr int64_t kWideRows = 8;
+
+// The forms with waves that split K (fewer row blocks than the forms with
+// shared fragments want): two row blocks per wave where that still gives every
 // CU two workgroups, counting every slot as used.
 struct Split {
   int ks, p;
 };
 Split choose_split(int64_t row_blocks, int64_t ktiles, int64_t slots, int cus) {
-  Split s{4, 1};
-  for (const Split c : {Split{1, 4}, Split{2, 4}, Split{4, 4}, Split{4, 2}}) {
-    if (c.ks <= ktiles && slots * (row_blocks / (4 / c.ks * c.p)) >= 2 * cus) {
-      s = c;
-      break;
-    }
-  }
+  Split s{4, slots * (row_blocks / 2) >= 2 * cus ? 2 : 1};
   while (s.ks > ktiles) s.ks >>= 1;
   return s;
 }
@@ -1049,9 +1106,8 @@ int launch_experts(const MoeCall& c, const double* logits, int renorm) {
   const _Float16* sc = c.gate_up_scales;
   _Float16 *hi = c.hi, *lo = c.lo, *Y = c.Y;
   float* part = c.part;
-  // The forms that share the token fragments, where they give every CU two workgroups.
   const int64_t wide_gu = static_cast<int64_t>(slots) * (s.I / 16), wide_dn = static_cast<int64_t>(slots) * (s.H / 16);
-  if (!logits && wide_gu >= 8 * cus) {
+  if (!logits && wide_gu >= kWideRows * cus) {
     const int p = wide_gu >= 16 * cus ? 2 : 1;
     void* args[] = {&X, &ids, &weights, &w, &sc, &hi, &lo, &s, &by_pair};
     const dim3 grid(static_cast<unsigned>(s.I / 16 / (4 * p)), grid_y, groups);
@@ -1067,13 +1123,11 @@ int launch_experts(const MoeCall& c, const double* logits, int renorm) {
     const dim3 grid(static_cast<unsigned>(s.I / 16 / (4 / sp.ks * sp.p)), grid_y, groups);
     const void* kern = nullptr;
     if (logits)
-      kern = sp.p == 4   ? reinterpret_cast<const void*>(&moe_gate_up<F, 4, 1, true>)
-             : sp.p == 2 ? reinterpret_cast<const void*>(&moe_gate_up<F, 2, 1, true>)
-                         : reinterpret_cast<const void*>(&moe_gate_up<F, 1, 2, true>);
+      kern = sp.p == 2 ? reinterpret_cast<const void*>(&moe_gate_up<F, 2, 1, true>)
+                       : reinterpret_cast<const void*>(&moe_gate_up<F, 1, 2, true>);
     else
-      kern = sp.p == 4   ? reinterpret_cast<const void*>(&moe_gate_up<F, 4, 1, false>)
-             : sp.p == 2 ? reinterpret_cast<const void*>(&moe_gate_up<F, 2, 1, false>)
-                         : reinterpret_cast<const void*>(&moe_gate_up<F, 1, 2, false>);
+      kern = sp.p == 2 ? reinterpret_cast<const void*>(&moe_gate_up<F, 2, 1, false>)
+                       : reinterpret_cast<const void*>(&moe_gate_up<F, 1, 2, false>);
     const int st = moe_launch(kern, grid, dim3(256), args, c.stream);
     if (st != FP6_OK) return st;
   }
@@ -1087,21 +1141,23 @@ int launch_experts(const MoeCall& c, const double* logits, int renorm) {
                       args, c.stream);
   }
   int st = FP6_OK;
-  if (wide_dn >= 16 * cus) {
-    const int p = !two && wide_dn >= 32 * cus ? 4 : 2;  // two column groups: no registers for four row blocks
+  if (wide_dn >= kWideRows * cus) {
+    // Four row blocks per wave leave no registers for two column groups.
+    const int p = wide_dn < 16 * cus ? 1 : (!two && wide_dn >= 32 * cus ? 4 : 2);
     void* args[] = {&hi, &lo, &ids, &w, &sc, &part, &s, &by_pair};
     const dim3 grid(static_cast<unsigned>(s.H / 16 / (4 * p)), grid_y, groups);
-    const void* kern = p == 4 ? reinterpret_cast<const void*>(&moe_down_wide<F, 4, 2, 1>)
-                              : (two ? reinterpret_cast<const void*>(&moe_down_wide<F, 2, 4, 2>)
+    const void* kern = p == 4   ? reinterpret_cast<const void*>(&moe_down_wide<F, 4, 2, 1>)
+                       : p == 1 ? (two ? reinterpret_cast<const void*>(&moe_down_wide<F, 1, 4, 2>)
+                                       : reinterpret_cast<const void*>(&moe_down_wide<F, 1, 4, 1>))
+                                : (two ? reinterpret_cast<const void*>(&moe_down_wide<F, 2, 4, 2>)
                                      : reinterpret_cast<const void*>(&moe_down_wide<F, 2, 4, 1>));
     st = moe_launch(kern, grid, dim3(256), args, c.stream);
   } else {
     Split sp = choose_split(s.H / 16, s.I / 256, slots, cus);
     void* args[] = {&hi, &lo, &ids, &w, &sc, &part, &s, &sp.ks, &by_pair};
     const dim3 grid(static_cast<unsigned>(s.H / 16 / (4 / sp.ks * sp.p)), grid_y, groups);
-    const void* kern = sp.p == 4   ? reinterpret_cast<const void*>(&moe_down<F, 4, 1>)
-                       : sp.p == 2 ? reinterpret_cast<const void*>(&moe_down<F, 2, 1>)
-                                   : reinterpret_cast<const void*>(&moe_down<F, 1, 2>);
+    const void* kern = sp.p == 2 ? reinterpret_cast<const void*>(&moe_down<F, 2, 1>)
+                                 : reinterpret_cast<const void*>(&moe_down<F, 1, 2>);
     st = moe_launch(kern, grid, dim3(256), args, c.stream);
   }
   if (st != FP6_OK) return st;
@@ -1215,7 +1271,11 @@ int fpx_moe_layer(int format, const void* X, const void* router, const void* gat
   const _Float16* R = static_cast<const _Float16*>(router);
   st = T <= 4 ? launch_logits<1>(c.X, R, logits, c.s, c.stream) : launch_logits<4>(c.X, R, logits, c.s, c.stream);
   if (st != FP6_OK) return st;
-  if (T <= kFusedT && E <= kFusedE) return launch_experts_format(format, c, logits, renormalize);
+  // The choice inside the first product, where that has few row blocks (the
+  // form with shared fragments expects it made).
+  const int64_t slots = T * top_k < E ? T * top_k : E;
+  if (T <= kFusedT && E <= kFusedE && slots * (I / 16) < kWideRows * fpx::current_cus())
+    return launch_experts_format(format, c, logits, renormalize);
   int* oi = static_cast<int*>(ids);
   float* ow = static_cast<float*>(weights);
   int E32 = c.s.E, k32 = c.s.k;
