@@ -58,9 +58,8 @@ int fp6_int8_quantize_rows(const float* W, int64_t N, int64_t K, int8_t* codes, 
  * A row that holds an infinity or a NaN gets scale NaN and zero codes, so that
  * every output of fp6_int8_linear for it is NaN.
  * dtype:  enum fp6_dtype of X.
- * X:      device [M] rows of K elements, row m at element m*ldx (ldx >= K).  No
- *         alignment beyond the element's own; rows that start at multiples of
- *         16 bytes are read faster.
+ * X:      device [M] rows of K elements, row m at element m*ldx (ldx >= K), at the
+ *         elements' own alignment.
  * Xq:     device int8 [M][Kp] out, 16-byte aligned, zero from K on.
  * scales: device float32 [M] out, 4-byte aligned.
  * M == 0 is a no-op.  Errors: FP6_E_VALUE (dtype), FP6_E_SHAPE (also ldx < K),

@@ -36,7 +36,9 @@ def _f64(t):
 # --- quantiser --------------------------------------------------------------
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("M,K,pad", [(1, 1, 0), (3, 7, 0), (2, 16, 8), (5, 17, 3), (4, 255, 1), (1, 1024, 0),
-                                     (7, 1025, 0), (33, 2048, 8), (3, 8192, 16), (2, 9001, 0), (1, 131056, 0)])
+                                     (7, 1025, 0), (33, 2048, 8), (3, 8192, 16), (2, 9001, 0), (1, 131056, 0),
+                                     (9, 512, 1), (6, 513, 0), (5, 2049, 3), (2, 4096, 5), (3, 4097, 0), (2, 16384, 0),
+                                     (2, 16385, 7)])
 def test_quantize_tokens(dtype, M, K, pad):
     X = _tokens(M, K, dtype, 100 * M + K, pad)
     q, s = fp6.int8_quantize_tokens(X)
@@ -147,8 +149,10 @@ def test_linear_largest_sum():
     assert torch.equal(Y.double().cpu(), (torch.tensor([[16384.0 * K, -16256.0 * K]]) * 2.0 ** -20).half().double().expand(3, 2))
 
 
-@pytest.mark.parametrize("M", [1, 7, 16, 40, 150, 300])
-@pytest.mark.parametrize("dtype,pad,K,N", [("fp16", 0, 1024, 512), ("bf16", 5, 1011, 77), ("fp16", 8, 333, 1000)])
+@pytest.mark.parametrize("M", [1, 2, 4, 5, 7, 16, 40, 150, 300])
+@pytest.mark.parametrize("dtype,pad,K,N", [("fp16", 0, 1024, 512), ("bf16", 5, 1011, 77), ("fp16", 8, 333, 1000),
+                                           ("fp16", 1, 8192, 40), ("bf16", 0, 4200, 33), ("fp16", 3, 1, 5),
+                                           ("bf16", 0, 8208, 24)])
 def test_linear_tokens_is_quantiser_then_product(M, dtype, pad, K, N):
     X = _tokens(M, K, dtype, M, pad)
     W, sw = fp6.int8_quantize_rows(np.random.default_rng(K).standard_normal((N, K)).astype(np.float32))
@@ -161,6 +165,15 @@ def test_linear_tokens_is_quantiser_then_product(M, dtype, pad, K, N):
     qr, sr = int8_codes(_f64(X))
     ref, bound = int8_product(qr, sr, _f64(W)[:, :K], _f64(sw), _f64(bias), dtype)
     assert (np.abs(_f64(Y) - ref) <= bound).all()
+
+
+def test_linear_tokens_zero_and_non_finite_rows():
+    W, sw = _codes((40, 1008), 3).to(DEV), torch.rand(40, device=DEV)
+    for M in (4, 9):
+        X = _tokens(M, 1000, "fp16", M)
+        X[1], X[2, 7], X[3, 999] = 0, float("nan"), float("-inf")
+        y = fp6.int8_linear(X, W, sw)
+        assert (y[1] == 0).all() and torch.isnan(y[2:4]).all() and torch.isfinite(y[0]).all()
 
 
 def test_linear_near_the_true_product():

@@ -89,21 +89,29 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
   return (a & 0xFF) | ((b & 0xFF) << 8) | ((c & 0xFF) << 16) | (static_cast<uint32_t>(d) << 24);
 }
 
-// One row per workgroup.  VEC: rows start at multiples of 16 bytes, 8 elements
-// per load; the last, partial unit of a row is read element by element.
-template <int DT, bool VEC>
-__global__ __launch_bounds__(256) void i8_quantize(const uint16_t* __restrict__ X, int64_t ldx, int K,
-                                                   int kp, int8_t* __restrict__ Q,
-                                                   float* __restrict__ scales) {
+// A row per wave (WAVES == 1, four rows per workgroup) or per workgroup of four
+// waves.  A thread's units of 8 elements (16 bytes, at any 2-byte alignment)
+// stay in registers between the maximum and the codes for rows of up to 8 *
+// UNITS * 64 * WAVES elements; longer rows (UNITS == 0) are read twice, the
+// second time from the caches.  Bound by the bytes of X and of the codes:
+// 4096x8192 bf16 18.6 us, 5.4 TB/s (25.1 us with a second read; rows that start
+// at odd elements 18.8 us, 64 us read element by element).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+template <int DT, int UNITS, int WAVES>
+__global__ __launch_bounds__(256) void i8_quantize(const uint16_t* __restrict__ X, int64_t ldx, int64_t M, int K, int kp,
+                                                   int8_t* __restrict__ Q, float* __restrict__ scales) {
   __shared__ uint32_t wtop[4];
-  const int tid = threadIdx.x, nthr = blockDim.x;
-  const int64_t m = blockIdx.x;
+  constexpr int kThreads = 64 * WAVES;
+  const int tid = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t m = WAVES == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (m >= M) return;  // WAVES == 1: no barrier below
   const uint16_t* x = X + m * ldx;
-  const int units = kp >> 3;  // of 8 elements
+  const int units = kp >> 3;
   auto load = [&](int u) -> u32x4 {
-    u32x4 v;
-    if (VEC && 8 * u + 8 <= K) {
-      v = *reinterpret_cast<const u32x4*>(x + 8 * u);
+    u32x4 v = {0, 0, 0, 0};
+    if (8 * u + 8 <= K) {
+      v = *reinterpret_cast<const u32x4_any*>(x + 8 * u);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -114,27 +122,40 @@ __global__ __launch_bounds__(256) void i8_quantize(const uint16_t* __restrict__ 
     return v;
   };
   uint32_t top = 0;
-  for (int u = tid; u < units; u += nthr) {
-    const u32x4 v = load(u);
+  auto look = [&](const u32x4& v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t lo = v[i] & 0x7FFFu, hi = (v[i] >> 16) & 0x7FFFu;
       top = lo > top ? lo : top;
       top = hi > top ? hi : top;
     }
+  };
+  u32x4 held[UNITS > 0 ? UNITS : 1];
+  if constexpr (UNITS > 0) {
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+      const int u = tid + i * kThreads;
+      held[i] = u < units ? load(u) : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) look(held[i]);
+  } else {
+    for (int u = tid; u < units; u += kThreads) look(load(u));
   }
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) {
     const uint32_t o = __shfl_xor(top, d);
     top = o > top ? o : top;
   }
-  if ((tid & 63) == 0) wtop[tid >> 6] = top;
-  __syncthreads();
-  for (int w = 0; w < (nthr >> 6); ++w) top = wtop[w] > top ? wtop[w] : top;
+  if constexpr (WAVES > 1) {
+    if ((tid & 63) == 0) wtop[tid >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) top = wtop[w] > top ? wtop[w] : top;
+  }
   const RowScale rs = row_scale_of(__builtin_bit_cast(uint32_t, Elem<DT>::to_float(top)));
   if (tid == 0) scales[m] = rs.s;
-  for (int u = tid; u < units; u += nthr) {
-    const u32x4 v = load(u);
+  auto store = [&](int u, const u32x4& v) {
     int q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -145,6 +166,15 @@ __global__ __launch_bounds__(256) void i8_quantize(const uint16_t* __restrict__ 
     o[0] = pack4(q[0], q[1], q[2], q[3]);
     o[1] = pack4(q[4], q[5], q[6], q[7]);
     *reinterpret_cast<u32x2*>(Q + m * kp + 8 * u) = o;
+  };
+  if constexpr (UNITS > 0) {
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+      const int u = tid + i * kThreads;
+      if (u < units) store(u, held[i]);
+    }
+  } else {
+    for (int u = tid; u < units; u += kThreads) store(u, load(u));
   }
 }
 
@@ -468,24 +498,147 @@ __global__ __launch_bounds__(64 * WA * WB * WK, 2) void i8_tiled(const int8_t* _
 }
 
 // ---------------------------------------------------------------------------
+// Quantiser and product in one kernel, for one token: a workgroup of 4 waves
+// owns 16 channels and makes the token's codes for itself, in LDS, while its
+// first weights are on their way; then the waves split K in contiguous parts
+// (weights straight into fragments; every MFMA column repeats the token) and
+// add their exact sums.  It saves the quantiser's launch and the codes' way
+// through memory: 1x4096x4096 7.6 us against 8.5 (in a graph; a launch less from
+// the host, too), 1x8192x8192 17.9 against 18.4.  With more tokens every
+// workgroup's own quantising costs more than it saves: 2x8192x2048 9.6 against
+// 9.0, 4x4096x4096 13.2 against 8.7.
+// ---------------------------------------------------------------------------
+constexpr int kOneTokenK = 8192;
+
+template <int DX, int DT>
+__global__ __launch_bounds__(256, 2) void i8_one_token(const uint16_t* __restrict__ x, int K,
+                                                       const int8_t* __restrict__ Wq, const float* __restrict__ sw,
+                                                       const void* __restrict__ bias, void* __restrict__ Y, int64_t N,
+                                                       int kp) {
+  constexpr int kWaves = 4, kBatch = 8;  // steps of 128 bytes in flight per wave
+  __shared__ i32x4 codes[kOneTokenK / 16];
+  __shared__ uint32_t wtop[kWaves];
+  __shared__ i32x4 red[kWaves][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int total = (kp + 127) >> 7;
+  const int t0 = wave * total / kWaves, t1 = (wave + 1) * total / kWaves;
+  const int8_t* w = Wq + (n0 + r < N ? n0 + r : N - 1) * kp;
+  i32x4 wf[2 * kBatch];
+  auto load_w = [&](int t) {  // half h of step t: bytes 128 t + 64 h + 16 g
+#pragma unroll
+    for (int i = 0; i < 2 * kBatch; ++i) {
+      const int k = (t + (i >> 1)) * 128 + (i & 1) * 64 + 16 * g;
+      wf[i] = *reinterpret_cast<const i32x4*>(w + (k < kp ? k : 0));  // behind the row: a stand-in, times zero
+    }
+  };
+  load_w(t0);
+
+  const int units = kp >> 3;  // of 8 elements
+  auto load_x = [&](int u) -> u32x4 {
+    u32x4 v = {0, 0, 0, 0};
+    if (8 * u + 8 <= K) {
+      v = *reinterpret_cast<const u32x4_any*>(x + 8 * u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = 8 * u + 2 * i;
+        v[i] = (k < K ? x[k] : 0u) | (k + 1 < K ? static_cast<uint32_t>(x[k + 1]) << 16 : 0u);
+      }
+    }
+    return v;
+  };
+  uint32_t top = 0;
+  for (int u = tid; u < units; u += 256) {
+    const u32x4 v = load_x(u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = v[i] & 0x7FFFu, hi = (v[i] >> 16) & 0x7FFFu;
+      top = lo > top ? lo : top;
+      top = hi > top ? hi : top;
+    }
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    const uint32_t o = __shfl_xor(top, d);
+    top = o > top ? o : top;
+  }
+  if (lane == 0) wtop[wave] = top;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kWaves; ++v) top = wtop[v] > top ? wtop[v] : top;
+  const RowScale rs = row_scale_of(__builtin_bit_cast(uint32_t, Elem<DX>::to_float(top)));
+  // The codes, with zeros up to whole steps.
+  for (int u = tid; u < 16 * total; u += 256) {
+    u32x2 o = {0, 0};
+    if (u < units) {
+      const u32x4 v = load_x(u);
+      int q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float f = Elem<DX>::to_float((v[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+        q[i] = rs.r == 0.0f ? 0 : quant1(f * rs.up, rs.r);
+      }
+      o[0] = pack4(q[0], q[1], q[2], q[3]);
+      o[1] = pack4(q[4], q[5], q[6], q[7]);
+    }
+    reinterpret_cast<u32x2*>(codes)[u] = o;
+  }
+  __syncthreads();
+
+  i32x4 acc = {0, 0, 0, 0};
+  for (int t = t0; t < t1; t += kBatch) {
+#pragma unroll
+    for (int i = 0; i < 2 * kBatch; ++i) {
+      if (t + (i >> 1) < t1)
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[i], codes[(t + (i >> 1)) * 8 + (i & 1) * 4 + g], acc, 0, 0, 0);
+    }
+    if (t + kBatch < t1) load_w(t + kBatch);
+  }
+  red[wave][lane] = acc;
+  __syncthreads();
+  if (wave == 0) {
+    i32x4 sum[1][1] = {{red[0][lane]}};
+#pragma unroll
+    for (int v = 1; v < kWaves; ++v) sum[0][0] += red[v][lane];
+    const int64_t n = n0 + 4 * g;
+    if (r == 0 && (N & 3) == 0 && n < N) store_tile<DT, 1, 1, true>(Y, sum, &rs.s, sw, bias, 0, n, 1, N);
+    else if (r == 0) store_tile<DT, 1, 1, false>(Y, sum, &rs.s, sw, bias, 0, n, 1, N);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool dtype_ok(int d) { return d == FP6_FP16 || d == FP6_BF16; }
 
-template <int DT, bool VEC>
+template <int DT>
 int launch_quantize_t(const void* X, int64_t ldx, int64_t M, int64_t K, void* Xq, void* scales, hipStream_t s) {
   int k = static_cast<int>(K), kp = static_cast<int>(fp6_int8_padded_k(K));
-  const int thr = kp <= 1024 ? 64 : 256;
+  const void* kern;
+  int rows = 1;  // per workgroup
+  if (kp <= 2048) {
+    rows = 4;
+    kern = kp <= 512    ? reinterpret_cast<const void*>(&i8_quantize<DT, 1, 1>)
+           : kp <= 1024 ? reinterpret_cast<const void*>(&i8_quantize<DT, 2, 1>)
+                        : reinterpret_cast<const void*>(&i8_quantize<DT, 4, 1>);
+  } else {
+    kern = kp <= 4096    ? reinterpret_cast<const void*>(&i8_quantize<DT, 2, 4>)
+           : kp <= 8192  ? reinterpret_cast<const void*>(&i8_quantize<DT, 4, 4>)
+           : kp <= 16384 ? reinterpret_cast<const void*>(&i8_quantize<DT, 8, 4>)
+                         : reinterpret_cast<const void*>(&i8_quantize<DT, 0, 4>);
+  }
   // A grid holds fewer than 2^32 threads: at most 2^22 rows per launch.
   constexpr int64_t kRows = int64_t(1) << 22;
   for (int64_t m0 = 0; m0 < M; m0 += kRows) {
     const uint16_t* x = static_cast<const uint16_t*>(X) + m0 * ldx;
     int8_t* q = static_cast<int8_t*>(Xq) + m0 * kp;
     float* sc = static_cast<float*>(scales) + m0;
-    void* args[] = {&x, &ldx, &k, &kp, &q, &sc};
-    const dim3 grid(static_cast<unsigned>(M - m0 < kRows ? M - m0 : kRows));
-    const int st = launch(reinterpret_cast<const void*>(&i8_quantize<DT, VEC>), grid, dim3(thr), args, s);
+    int64_t n = M - m0 < kRows ? M - m0 : kRows;
+    void* args[] = {&x, &ldx, &n, &k, &kp, &q, &sc};
+    const int st = launch(kern, dim3(static_cast<unsigned>(ceil_div(n, rows))), dim3(256), args, s);
     if (st != FP6_OK) return st;
   }
   return FP6_OK;
@@ -493,12 +646,8 @@ int launch_quantize_t(const void* X, int64_t ldx, int64_t M, int64_t K, void* Xq
 
 int launch_quantize(int dtype, const void* X, int64_t ldx, int64_t M, int64_t K, void* Xq, void* scales,
                     hipStream_t s) {
-  const bool vec = aligned(X, 16) && ldx % 8 == 0;
-  if (dtype == FP6_FP16)
-    return vec ? launch_quantize_t<FP6_FP16, true>(X, ldx, M, K, Xq, scales, s)
-               : launch_quantize_t<FP6_FP16, false>(X, ldx, M, K, Xq, scales, s);
-  return vec ? launch_quantize_t<FP6_BF16, true>(X, ldx, M, K, Xq, scales, s)
-             : launch_quantize_t<FP6_BF16, false>(X, ldx, M, K, Xq, scales, s);
+  return dtype == FP6_FP16 ? launch_quantize_t<FP6_FP16>(X, ldx, M, K, Xq, scales, s)
+                           : launch_quantize_t<FP6_BF16>(X, ldx, M, K, Xq, scales, s);
 }
 
 struct Product {
@@ -607,6 +756,21 @@ int launch_product(int dtype, const Product& p, int variant, hipStream_t s) {
   return dtype == FP6_FP16 ? launch_product_t<FP6_FP16>(p, variant, s) : launch_product_t<FP6_BF16>(p, variant, s);
 }
 
+template <int DX>
+int launch_one_token(const void* X, int64_t K, const Product& p, int dtype, hipStream_t s) {
+  const uint16_t* x = static_cast<const uint16_t*>(X);
+  const int8_t* w = static_cast<const int8_t*>(p.wq);
+  const float* sw = static_cast<const float*>(p.sw);
+  const void* bias = p.bias;
+  void* y = p.y;
+  int k = static_cast<int>(K), kp = static_cast<int>(p.kp);
+  int64_t N = p.N;
+  void* args[] = {&x, &k, &w, &sw, &bias, &y, &N, &kp};
+  const void* kern = dtype == FP6_FP16 ? reinterpret_cast<const void*>(&i8_one_token<DX, FP6_FP16>)
+                                       : reinterpret_cast<const void*>(&i8_one_token<DX, FP6_BF16>);
+  return launch(kern, dim3(static_cast<unsigned>(ceil_div(N, 16))), dim3(256), args, s);
+}
+
 bool sizes_ok(int64_t M, int64_t N, int64_t kp) {
   return M >= 0 && M <= fp6::kMaxDim && N >= 1 && N <= fp6::kMaxDim && N * kp <= fp6::kMaxNK &&
          M * kp <= fp6::kMaxNK && M * N <= fp6::kMaxNK;
@@ -659,6 +823,12 @@ int fp6_int8_linear_tokens(int x_dtype, const void* X, int64_t ldx, const void* 
   int8_t* xq = static_cast<int8_t*>(workspace);
   float* sx = reinterpret_cast<float*>(xq + M * kp);  // M*kp is a multiple of 16
   const hipStream_t s = static_cast<hipStream_t>(stream);
+  // Every workgroup reads X: for up to two of them per CU.
+  if (M == 1 && kp <= kOneTokenK && ceil_div(N, 16) <= 2 * fpx::current_cus()) {
+    const Product p{nullptr, nullptr, Wq, sw, bias, Y, M, N, kp};
+    return x_dtype == FP6_FP16 ? launch_one_token<FP6_FP16>(X, K, p, dtype, s)
+                               : launch_one_token<FP6_BF16>(X, K, p, dtype, s);
+  }
   const int st = launch_quantize(x_dtype, X, ldx, M, K, xq, sx, s);
   if (st != FP6_OK) return st;
   return launch_product(dtype, Product{xq, sx, Wq, sw, bias, Y, M, N, kp}, kAuto, s);
