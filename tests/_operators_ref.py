@@ -3,8 +3,6 @@ mixture-of-experts layer, shared by their tests (NumPy only)."""
 
 import numpy as np
 
-import oracle
-
 HALF_STEP = {"fp16": 2.0 ** -11, "bf16": 2.0 ** -8}    # one rounding, relative
 TINY = {"fp16": 2.0 ** -25, "bf16": 2.0 ** -134}       # half a subnormal step
 U32 = 2.0 ** -24
@@ -30,10 +28,6 @@ def int8_product(q, sx, w, sw, bias, out):
     y = p + b
     slack = 4 * U32 * (np.abs(p) + np.abs(b)) * 1.01
     return y, slack + HALF_STEP[out] * (np.abs(y) + slack) + TINY[out]
-
-
-def experts_dequant(codes, scales, fmt):
-    return np.stack([oracle.dequant_ref(c, s, fmt).astype(np.float64) for c, s in zip(codes, scales)])
 
 
 def route(x, router, k, renormalize):
@@ -64,22 +58,26 @@ def experts(x, ids, weights, w13, w2, weight_bound=None):
     T, H = x.shape
     E, I = w13.shape[0], w13.shape[1] // 2
     y, slack = np.zeros((T, H)), np.zeros((T, H))
-    for t in range(T):
-        served = sorted({int(e) for e in ids[t] if 0 <= e < E})
-        for e in served:
+    many = [len({int(e) for e in ids[t] if 0 <= e < E}) for t in range(T)]
+    for e in sorted({int(e) for e in np.asarray(ids).ravel() if 0 <= e < E}):
+        up, down = w13[e], w2[e]
+        aup, adown = np.abs(up), np.abs(down)
+        for t in range(T):
             hit = [j for j in range(ids.shape[1]) if ids[t, j] == e]
+            if not hit:
+                continue
             wt = weights[t, hit].sum()
             dw = len(hit) * U32 * np.abs(weights[t, hit]).sum()
             if weight_bound is not None:
                 dw += weight_bound[t, hit].sum()
-            gu = w13[e] @ x[t]
-            d = H * U32 * (np.abs(w13[e]) @ np.abs(x[t]))
+            gu = up @ x[t]
+            d = H * U32 * (aup @ np.abs(x[t]))
             g, u, dg, du = gu[:I], gu[I:], d[:I], d[I:]
             act = g / (1 + np.exp(-g))
             h = act * u * wt
             dh = ((1.1 * dg + 8 * U32 * np.abs(act)) * (np.abs(u) + du) + np.abs(act) * du) * (abs(wt) + dw)
             dh += np.abs(act * u) * dw + (4 * U32 + 2.0 ** -22) * np.abs(h) + 2.0 ** -28
-            y[t] += w2[e] @ h
-            n = I * len(served) + 64
-            slack[t] += np.abs(w2[e]) @ dh + n * U32 * (np.abs(w2[e]) @ (np.abs(h) + dh))
+            y[t] += down @ h
+            n = I * many[t] + 64
+            slack[t] += adown @ dh + n * U32 * (adown @ (np.abs(h) + dh))
     return y, slack + HALF_STEP["fp16"] * (np.abs(y) + slack) + TINY["fp16"]

@@ -3,7 +3,9 @@
 import numpy as np
 import pytest
 
-from _operators_ref import experts, experts_dequant, int8_codes, int8_product, route
+import oracle
+
+from _operators_ref import experts, int8_codes, int8_product, route
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -17,8 +19,18 @@ DEV = torch.device("cuda:0")
 _cache = {}
 
 
+class Dequantised:
+    """The experts' matrices in float64, each made when it is asked for."""
+
+    def __init__(self, codes, scales, fmt):
+        self.codes, self.scales, self.fmt, self.shape = codes, scales, fmt, codes.shape
+
+    def __getitem__(self, e):
+        return oracle.dequant_ref(self.codes[e], self.scales[e], self.fmt).astype(np.float64)
+
+
 class Experts:
-    """A stack of random experts, packed on the GPU and de-quantised in float64."""
+    """A stack of random experts, packed on the GPU."""
 
     def __init__(self, E, H, I, fmt="e3m2", seed=0):
         rng = np.random.default_rng(seed + E + H + I)
@@ -30,7 +42,7 @@ class Experts:
             top = {"e3m2": 28.0, "e2m3": 7.5, "e2m2": 7.0, "e2m1": 6.0}[fmt]
             scales = (rng.uniform(2, 4, (E, rows)) / top / cols ** 0.5).astype(np.float16)
             self.args += [torch.from_numpy(fp6.moe_prepack(codes, scales, fmt)).to(DEV), torch.from_numpy(scales).to(DEV)]
-            self.dq.append(experts_dequant(codes, scales, fmt))
+            self.dq.append(Dequantised(codes, scales, fmt))
 
     @classmethod
     def get(cls, *key):
@@ -94,6 +106,28 @@ def test_experts_many_and_top_k_16():
     ex = Experts.get(512, 256, 256, "e2m1")
     _run(ex, _x(2, 256, 1), *_routing(2, 512, 16, 1))
     _run(ex, _x(40, 256, 2), *_routing(40, 512, 16, 2))
+
+
+@pytest.mark.parametrize("fmt", ["e3m2", "e2m3", "e2m2", "e2m1"])
+@pytest.mark.parametrize("E,H,I", [(64, 512, 512), (128, 512, 512), (256, 512, 256), (128, 256, 1280)])
+def test_experts_many_row_blocks(fmt, E, H, I):
+    # The forms that share token fragments: every expert count per CU, up to 16 tokens and more.
+    ex = Experts(E, H, I, fmt)
+    _run(ex, _x(16, H, 1), *_routing(16, E, 16, 1))
+    _run(ex, _x(20, H, 2), *_routing(20, E, 13, 2))
+
+
+@pytest.mark.parametrize("E,H,I", [(64, 512, 512), (128, 512, 256), (6, 512, 512)])
+def test_experts_uneven_routing(E, H, I):
+    # One expert chosen by every token, one by 33, one by 32, one by 17, one by 16, the rest spread.
+    ex = Experts.get(E, H, I)
+    T, k = 64, 6
+    rng = np.random.default_rng(5)
+    ids = np.stack([np.concatenate([[3], rng.integers(0, E, k - 1)]) for _ in range(T)]).astype(np.int32)
+    for j, (e, n) in enumerate([(1, 33), (0, 32), (4, 17), (5, 16)]):
+        ids[:, 1 + j] = np.where(rng.permutation(T) < n, e, ids[:, 1 + j])
+    w = rng.dirichlet(np.ones(k), T).astype(np.float32)
+    _run(ex, _x(T, H, 1), torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV))
 
 
 def test_experts_same_index_twice():
@@ -186,10 +220,10 @@ def test_layer(T, E, k, renormalize):
     assert torch.equal(y, y2)
 
 
-@pytest.mark.parametrize("E,k", [(1, 1), (7, 7), (65, 3), (200, 16), (512, 8)])
+@pytest.mark.parametrize("E,k", [(1, 1), (7, 7), (65, 3), (128, 5), (129, 5), (200, 16), (512, 8)])
 def test_layer_many_experts(E, k):
     ex = Experts.get(E, 256, 256, "e2m1")
-    for T in (1, 3, 20):
+    for T in (1, 3, 4, 20):
         X, router = _x(T, 256, T), _x(E, 256, 7) * 0.2
         y, ids, w = fp6.moe_layer(X, router, *ex.args, top_k=k, fmt="e2m1")
         rid, rw, rb = route(_f64(X), _f64(router), k, True)
