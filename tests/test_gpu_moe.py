@@ -232,6 +232,23 @@ def test_layer_many_experts(E, k):
         _check(y, *experts(_f64(X), rid, rw, *ex.dq, weight_bound=rb))
 
 
+@pytest.mark.parametrize("fmt", ["e3m2", "e2m3", "e2m2", "e2m1"])
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 2, 2048, 256), (1, 9, 2, 2048, 256), (4, 4, 1, 1024, 256), (3, 5, 2, 1024, 256),
+                                       (1, 64, 6, 256, 256), (1, 65, 6, 256, 256), (2, 4, 2, 256, 8192), (4, 17, 2, 256, 8192)])
+def test_layer_small_router(T, E, k, H, I, fmt):
+    """Both sides of the size up to which the first product takes the router
+    itself, with few and many row blocks; equal router rows tie either way."""
+    ex = Experts.get(E, H, I, fmt)
+    X, router = _x(T, H, T), _x(E, H, 7) * (0.1 if H < 2048 else 0.03)
+    router[E - 1] = router[0]
+    y, ids, w = fp6.moe_layer(X, router, *ex.args, top_k=k, fmt=fmt)
+    rid, rw, rb = route(_f64(X), _f64(router), k, True)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    assert (np.abs(_f64(w) - rw) <= rb).all()
+    _check(y, *experts(_f64(X), rid, rw, *ex.dq, weight_bound=rb))
+    assert torch.equal(y, fp6.moe_experts(X, ids, w, *ex.args, fmt=fmt))
+
+
 def test_layer_ties_go_to_the_lower_index():
     ex = Experts.get(6, 512, 512)
     router = _x(6, 512, 3) * 0.1
