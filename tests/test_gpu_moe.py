@@ -117,6 +117,18 @@ def test_experts_many_row_blocks(fmt, E, H, I):
     _run(ex, _x(20, H, 2), *_routing(20, E, 13, 2))
 
 
+@pytest.mark.parametrize("fmt", ["e3m2", "e2m2", "e2m1"])
+@pytest.mark.parametrize("H,I", [(256, 1280), (512, 1024), (768, 768), (1024, 512), (1280, 256), (2304, 256)])
+def test_experts_shared_fragments_every_depth(H, I, fmt):
+    # Fewer k-tiles than the ring of weights holds, whole turns of it and rests,
+    # with one and two groups of columns and a second pass (expert 3 gets all).
+    ex = Experts(128, H, I, fmt)
+    for T in (16, 33, 64):
+        ids, w = _routing(T, 128, 16, H + T)
+        ids[:, 0] = 3
+        _run(ex, _x(T, H, T + H), ids, w)
+
+
 @pytest.mark.parametrize("E,H,I", [(64, 512, 512), (128, 512, 256), (6, 512, 512)])
 def test_experts_uneven_routing(E, H, I):
     # One expert chosen by every token, one by 33, one by 32, one by 17, one by 16, the rest spread.
@@ -247,6 +259,20 @@ def test_layer_small_router(T, E, k, H, I, fmt):
     assert (np.abs(_f64(w) - rw) <= rb).all()
     _check(y, *experts(_f64(X), rid, rw, *ex.dq, weight_bound=rb))
     assert torch.equal(y, fp6.moe_experts(X, ids, w, *ex.args, fmt=fmt))
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(5, 8, 2, 512, 256), (17, 128, 3, 512, 256), (16, 129, 3, 256, 256), (6, 16, 4, 4096, 256),
+                                       (6, 17, 4, 4096, 256), (1024, 4, 2, 256, 256), (1025, 4, 2, 256, 256)])
+def test_layer_choice_in_one_or_two_launches(T, E, k, H, I):
+    """Both sides of the sizes up to which a token's logits and choice are one kernel."""
+    ex = Experts.get(E, H, I, "e2m1")
+    X, router = _x(T, H, T), _x(E, H, 7) * (0.1 if H < 2048 else 0.03)
+    router[E - 1] = router[1]
+    y, ids, w = fp6.moe_layer(X, router, *ex.args, top_k=k, fmt="e2m1")
+    rid, rw, rb = route(_f64(X), _f64(router), k, True)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    assert (np.abs(_f64(w) - rw) <= rb).all()
+    _check(y, *experts(_f64(X), rid, rw, *ex.dq, weight_bound=rb))
 
 
 def test_layer_ties_go_to_the_lower_index():

@@ -34,6 +34,11 @@ constexpr float kHScale = 0x1p-8f, kLoScale = 0x1p11f;
 // instead of 11.4, 16384 13.8 instead of 13.2, 32768 16.5 .. 18.7 instead of
 // 12.3 .. 15.1: every workgroup pays for all of them.
 constexpr int kFusedE = 128, kFusedT = 4, kFusedProducts = 16384;
+// More tokens: up to which router (experts x H) one workgroup per token makes
+// logits and choice in one launch instead of two.  8 experts x 1024: 16 tokens
+// 17.6 -> 15.3 us for the layer, 256 29.3 -> 26.7, 1024 73.8 -> 71.1; 16 x 4096:
+// 24.0 -> 23.6, 60.4 -> 58.6, 185 -> 181; 32 x 4096, 16 tokens 30.0 -> 32.5.
+constexpr int kRouteE = 128, kRouteProducts = 65536;
 enum Route : int { kGiven, kFromLogits, kFromRouter };
 constexpr int kFewPairs = 64, kFewTiles = 32;  // moe_down_few: a lane per pair, two tiles per wave
 
@@ -141,6 +146,42 @@ __global__ __launch_bounds__(64) void moe_topk(const double* __restrict__ logits
   if (lane < k) {
     ids[t * k + lane] = id;
     weights[t * k + lane] = w;
+  }
+}
+
+// Logits and choice of one token in one workgroup of 16 waves, for small routers.
+__global__ __launch_bounds__(1024) void moe_route(const _Float16* __restrict__ X, const _Float16* __restrict__ R, int E,
+                                                  int k, int H, int renorm, int* __restrict__ ids,
+                                                  float* __restrict__ weights) {
+  __shared__ double logits[kRouteE];
+  __shared__ uint64_t keys[kRouteE];
+  __shared__ int best[kMaxK];
+  __shared__ double best_l[kMaxK];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x;
+  const half8v* x = reinterpret_cast<const half8v*>(X + t * H);
+  for (int e = wave; e < E; e += 16) {
+    const half8v* w = reinterpret_cast<const half8v*>(R + static_cast<int64_t>(e) * H);
+    double acc = 0.0;
+#pragma unroll 4
+    for (int u = lane; u < H / 8; u += 64) {
+      const half8v wv = w[u], xv = x[u];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc += static_cast<double>(static_cast<float>(wv[i]) * static_cast<float>(xv[i]));
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) acc += __shfl_xor(acc, d);
+    if (lane == 0) logits[e] = acc;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    int id;
+    float w;
+    wave_topk(logits, E, k, renorm, keys, best, best_l, lane, id, w);
+    if (lane < k) {
+      ids[t * k + lane] = id;
+      weights[t * k + lane] = w;
+    }
   }
 }
 
@@ -436,30 +477,6 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up(const _Float16* __restrict
 // add instead of a kernel of its own: 64 tokens, 64 experts 2048x1024 181 us
 // against 37.)
 // ---------------------------------------------------------------------------
-template <typename LOAD>
-__device__ __forceinline__ void sum_choices(const int* __restrict__ ids, const MoeShape& s, LOAD load, _Float16* y) {
-  float4v v[kMaxK];
-  int id[kMaxK];
-#pragma unroll
-  for (int j = 0; j < kMaxK; ++j) id[j] = j < s.k ? ids[j] : -1;
-#pragma unroll
-  for (int j = 0; j < kMaxK; ++j) {
-    bool use = id[j] >= 0 && id[j] < s.E;
-#pragma unroll
-    for (int o = 0; o < j; ++o) use = use && id[o] != id[j];  // the same expert again: counted with the first
-    v[j] = float4v{0.f, 0.f, 0.f, 0.f};
-    if (use) v[j] = load(j);
-  }
-  float4v sum = v[0];
-#pragma unroll
-  for (int j = 1; j < kMaxK; ++j)
-    if (j < s.k) sum += v[j];
-  half4v o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = static_cast<_Float16>(sum[i] * (1.0f / kHScale));
-  *reinterpret_cast<half4v*>(y) = o;
-}
-
 template <int F, int P, int D>
 __global__ __launch_bounds__(256, 2) void moe_down(const _Float16* __restrict__ hi, const _Float16* __restrict__ lo,
                                                 const int* __restrict__ ids_g, const u32x4* __restrict__ wp,
@@ -580,23 +597,37 @@ __global__ __launch_bounds__(256, 2) void moe_down(const _Float16* __restrict__ 
 // k-tiles): one wave's fragments of a k-tile are 8 KB (h: 16 KB), more than its
 // weights, and come once per workgroup instead of once per wave.
 //
-// LDS buffer of a k-tile (two of them, filled by direct LDS loads one k-tile
-// ahead): 16 columns x 32 units of 16 bytes, unit u of column c at place
-// u ^ (c % 8), so that eight columns' reads of one unit cover a 128-byte line.
-// Per k-tile: wait for this wave's direct loads (a fixed count of weight loads
-// may still be in flight behind them), barrier, request the next k-tile's
-// columns, multiply, request the weights of k-tile t+D.
+// LDS buffer of a k-tile (one of D, filled by direct LDS loads): 16 columns x 32
+// units of 16 bytes, unit u of column c at place u ^ c, so that 16 columns'
+// reads of one unit cover all banks.
+//
+// Per k-tile t: wait for its columns, barrier (everybody's are there, and k-tile
+// t-1's buffer is free), request the columns of k-tile t+D-1, multiply, request
+// the weights of k-tile t+D.  Every k-tile issues the same loads, those behind
+// the last one from one address: the waits, the compiler's own among them, are
+// then fixed counts with D-1 k-tiles of weights and D-2 of columns in flight
+// behind.  (With the requests under conditions the compiler waited for all of
+// them in one k-tile of D: 64 tokens, 64 experts 2048x1024 gate/up 42.5 us and
+// down 32.4 instead of 40.3 and 26.6, 5.0 and 3.8 TB/s of weights.)
 // ---------------------------------------------------------------------------
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
 
+// A loaded value, waited for here: behind the first direct load the compiler
+// waits for every load before it uses one.
+__device__ __forceinline__ half2v landed(half2v v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // Direct loads of one k-tile of 16 columns by 4 waves: wave w fills units
-// [128 w, 128 w + 128); src[i]: this lane's source of unit 128 w + 64 i + lane.
-__device__ __forceinline__ void load_columns(half8v* buf, const _Float16* const (&src)[2], int kt, int wave) {
+// [128 w, 128 w + 128); at[i]: where this lane's part of the column of unit
+// 128 w + 64 i + lane begins, in bytes behind x (below 2^31: 1024 rows of 2^20).
+__device__ __forceinline__ void load_columns(half8v* buf, const _Float16* x, const uint32_t (&at)[2], int wave) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) lds_load<16>(src[i] + kt * 256, buf + 128 * wave + 64 * i);
+  for (int i = 0; i < 2; ++i) lds_load<16>(reinterpret_cast<const char*>(x) + at[i], buf + 128 * wave + 64 * i);
 }
 
 template <int F, int P, int D, int NC>
@@ -605,10 +636,11 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up_wide(const _Float16* __res
                                                         const u32x4* __restrict__ wp,
                                                         const _Float16* __restrict__ scales, _Float16* __restrict__ hi,
                                                         _Float16* __restrict__ lo, MoeShape s, int by_pair) {
-  static_assert(D % 2 == 0, "two column buffers");
+  static_assert(D == 2 || D == 4, "column buffers");
   __shared__ short col_token[4][kGroup], col_pair[4][kGroup];
   __shared__ float col_w[4][kGroup];
-  __shared__ half8v buf0[512 * NC], buf1[512 * NC];
+  // One array each: the compiler orders direct loads and reads of one array.
+  __shared__ half8v buf0[512 * NC], buf1[512 * NC], buf2[D > 2 ? 512 * NC : 1], buf3[D > 2 ? 512 * NC : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int t0 = blockIdx.z * kGroup;
@@ -625,8 +657,8 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up_wide(const _Float16* __res
   const int iblocks = s.I >> 4, ktiles = s.H >> 8;
   const int nb = (blockIdx.x * 4 + wave) * P;
   const int64_t kstr = 2 * static_cast<int64_t>(iblocks) * Fmt<F>::kTileQuads;
-  const u32x4* wg = wp + static_cast<int64_t>(e) * ktiles * kstr + nb * static_cast<int64_t>(Fmt<F>::kTileQuads) + lane;
-  const u32x4* wu = wg + static_cast<int64_t>(iblocks) * Fmt<F>::kTileQuads;
+  int64_t wg = static_cast<int64_t>(e) * ktiles * kstr + nb * static_cast<int64_t>(Fmt<F>::kTileQuads);
+  int64_t wu = wg + static_cast<int64_t>(iblocks) * Fmt<F>::kTileQuads;
   _Float16 sg[P], su[P];
   const _Float16* sc = scales + static_cast<int64_t>(e) * 2 * s.I + nb * 16 + r;
 #pragma unroll
@@ -637,17 +669,17 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up_wide(const _Float16* __res
   typename Fmt<F>::Tile tg[D][P], tu[D][P];
   constexpr int kW = 2 * P * Fmt<F>::kTileLoads;  // weight loads per k-tile
   auto load_w = [&](int slot_, int kt) {
+    const bool in = kt < ktiles;
+    const u32x4* pg = wp + (in ? wg + kt * kstr : 0);
+    const u32x4* pu = wp + (in ? wu + kt * kstr : 0);
+    const unsigned l = in ? lane : 0;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      Fmt<F>::template load<true>(tg[slot_][p], wg + kt * kstr + p * Fmt<F>::kTileQuads, lane);
-      Fmt<F>::template load<true>(tu[slot_][p], wu + kt * kstr + p * Fmt<F>::kTileQuads, lane);
+      Fmt<F>::template load<true>(tg[slot_][p], pg + p * Fmt<F>::kTileQuads + l, l);
+      Fmt<F>::template load<true>(tu[slot_][p], pu + p * Fmt<F>::kTileQuads + l, l);
     }
   };
-  auto load_ring = [&]() {
-#pragma unroll
-    for (int d = 0; d < D; ++d) load_w(d, d < ktiles ? d : 0);
-  };
-  load_ring();
+  load_w(0, 0);
   const uint64_t mask = __ballot(ch.first >= 0);
   if (!has_work(mask, ch.first, by_pair, slot)) return;
   const int n = __popcll(mask);
@@ -658,49 +690,65 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up_wide(const _Float16* __res
     col_w[wave][c] = ch.weight;
   }
   __builtin_amdgcn_wave_barrier();
+  half2v s2g[P], s2u[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    s2g[p] = landed(scale2_of<F>(sg[p]));
+    s2u[p] = landed(scale2_of<F>(su[p]));
+  }
   // One pass: C groups of 16 columns, from column c0 on.
   auto pass = [&](int c0, auto C) {
     constexpr int nc = decltype(C)::value;
-    const _Float16* src[nc][2];
+    // Every pass loads its weights itself, at its places in the order.
+    asm volatile("" : "+s"(wg), "+s"(wu));
+    uint32_t at[nc][2];
+    const _Float16* const Xg = X + static_cast<int64_t>(t0) * s.H;
 #pragma unroll
     for (int q = 0; q < nc; ++q)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int col = 4 * wave + 2 * i + (lane >> 5), c = c0 + 16 * q + col;
-        src[q][i] = X + static_cast<int64_t>(t0 + col_token[wave][c < n ? c : c0]) * s.H + 8 * ((lane & 31) ^ (col & 7));
+        at[q][i] = 2 * (col_token[wave][c < n ? c : c0] * static_cast<uint32_t>(s.H) + 8 * ((lane & 31) ^ col));
       }
     auto columns = [&](half8v* buf, int kt) {
+      const _Float16* x = Xg + (kt < ktiles ? kt * 256 : 0);
 #pragma unroll
-      for (int q = 0; q < nc; ++q) load_columns(buf + 512 * q, src[q], kt, wave);
+      for (int q = 0; q < nc; ++q) load_columns(buf + 512 * q, x, at[q], wave);
     };
+    // In the order of the loop, which its counts rely on.
     columns(buf0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(1, 1);
+    if constexpr (D > 2) {
+      __builtin_amdgcn_sched_barrier(0);
+      columns(buf1, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      load_w(2, 2);
+      __builtin_amdgcn_sched_barrier(0);
+      columns(buf2, 2);
+      __builtin_amdgcn_sched_barrier(0);
+      load_w(3, 3);
+    }
     __builtin_amdgcn_sched_barrier(0);
     float4v ag[nc][P], au[nc][P];
 #pragma unroll
     for (int q = 0; q < nc; ++q)
 #pragma unroll
       for (int p = 0; p < P; ++p) ag[q][p] = au[q][p] = float4v{0.f, 0.f, 0.f, 0.f};
-    auto tile = [&](int kt, auto U) {
+    auto tile = [&](int kt, auto U, auto W) {
       constexpr int u = decltype(U)::value;
-      const half8v* cur = u & 1 ? buf1 : buf0;
+      const half8v* cur = u == 0 ? buf0 : u == 1 ? buf1 : u == 2 ? buf2 : buf3;
+      half8v* next = (u + D - 1) % D == 0 ? buf0 : (u + D - 1) % D == 1 ? buf1 : (u + D - 1) % D == 2 ? buf2 : buf3;
       __builtin_amdgcn_sched_barrier(0);
-      // Behind this k-tile's columns: the weights of k-tile t-1+D, if any.
-      if (kt > 0 && kt - 1 + D < ktiles) wait_vm<kW>();
-      else wait_vm<0>();
+      wait_vm<decltype(W)::value * kW + (D - 2) * 2 * nc>();
       barrier_no_fence();
-      if (kt + 1 < ktiles) columns(u & 1 ? buf0 : buf1, kt + 1);
+      columns(next, kt + D - 1);
       __builtin_amdgcn_sched_barrier(0);
-      half2v s2g[P], s2u[P];
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        s2g[p] = scale2_of<F>(sg[p]);
-        s2u[p] = scale2_of<F>(su[p]);
-      }
       auto step = [&](auto J) {
         constexpr int j = decltype(J)::value;
         half8v x[nc];
 #pragma unroll
-        for (int q = 0; q < nc; ++q) x[q] = cur[512 * q + r * 32 + ((4 * j + g) ^ (r & 7))];
+        for (int q = 0; q < nc; ++q) x[q] = cur[512 * q + r * 32 + ((4 * j + g) ^ r)];
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           const half8v a = Fmt<F>::template step<j>(tg[u][p], s2g[p]), b = Fmt<F>::template step<j>(tu[u][p], s2u[p]);
@@ -716,16 +764,29 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up_wide(const _Float16* __res
       step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
       step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
       __builtin_amdgcn_sched_barrier(0);
-      if (kt + D < ktiles) load_w(u, kt + D);
     };
-    for (int kt = 0; kt < ktiles; kt += D) {
-      tile(kt, std::integral_constant<int, 0>{});
-      if (kt + 1 < ktiles) tile(kt + 1, std::integral_constant<int, 1>{});
+    auto turn = [&](int kt, auto U) {
+      tile(kt, U, std::integral_constant<int, D - 1>{});
+      load_w(decltype(U)::value, kt + D);
+    };
+    int kt = 0;
+    for (; kt + D <= ktiles; kt += D) {
+      turn(kt, std::integral_constant<int, 0>{});
+      turn(kt + 1, std::integral_constant<int, 1>{});
       if constexpr (D > 2) {
-        if (kt + 2 < ktiles) tile(kt + 2, std::integral_constant<int, 2>{});
-        if (kt + 3 < ktiles) tile(kt + 3, std::integral_constant<int, 3>{});
+        turn(kt + 2, std::integral_constant<int, 2>{});
+        turn(kt + 3, std::integral_constant<int, 3>{});
       }
     }
+    // The rest: no weights are requested any more, or, with fewer than D k-tiles
+    // in all, not all of the ring's were.
+    constexpr std::integral_constant<int, 0> kNone{};
+    if (kt < ktiles) tile(kt, std::integral_constant<int, 0>{}, kNone);
+    if constexpr (D > 2) {
+      if (kt + 1 < ktiles) tile(kt + 1, std::integral_constant<int, 1>{}, kNone);
+      if (kt + 2 < ktiles) tile(kt + 2, std::integral_constant<int, 2>{}, kNone);
+    }
+    wait_vm<0>();  // no load into the buffers outlives its pass
 #pragma unroll
     for (int q = 0; q < nc; ++q) {
       const int c = c0 + 16 * q + r;
@@ -741,7 +802,7 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up_wide(const _Float16* __res
     for (; n - c0 > 16; c0 += 32) {
       pass(c0, std::integral_constant<int, 2>{});
       __syncthreads();  // the buffers are free again
-      if (n - c0 > 32) load_ring();
+      if (n - c0 > 32) load_w(0, 0);
     }
     if (c0 < n) pass(c0, std::integral_constant<int, 1>{});
   } else {
@@ -754,9 +815,10 @@ __global__ __launch_bounds__(256, 2) void moe_down_wide(const _Float16* __restri
                                                      const int* __restrict__ ids_g, const u32x4* __restrict__ wp,
                                                      const _Float16* __restrict__ scales, float* __restrict__ part,
                                                      MoeShape s, int by_pair) {
-  static_assert(D % 2 == 0, "two column buffers");
+  static_assert(D == 2 || D == 4, "column buffers");
   __shared__ short col_pair[4][kGroup];
-  __shared__ half8v bufh0[512 * NC], bufh1[512 * NC], bufl0[512 * NC], bufl1[512 * NC];
+  // The columns' upper halves, and the lower ones behind them.
+  __shared__ half8v buf0[1024 * NC], buf1[1024 * NC], buf2[D > 2 ? 1024 * NC : 1], buf3[D > 2 ? 1024 * NC : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int t0 = blockIdx.z * kGroup;
@@ -773,7 +835,7 @@ __global__ __launch_bounds__(256, 2) void moe_down_wide(const _Float16* __restri
   const int ktiles = s.I >> 8;
   const int nb = (blockIdx.x * 4 + wave) * P;
   const int64_t kstr = static_cast<int64_t>(s.H >> 4) * Fmt<F>::kTileQuads;
-  const u32x4* w = wp + static_cast<int64_t>(e) * ktiles * kstr + nb * static_cast<int64_t>(Fmt<F>::kTileQuads) + lane;
+  int64_t w = static_cast<int64_t>(e) * ktiles * kstr + nb * static_cast<int64_t>(Fmt<F>::kTileQuads);
   _Float16 sw[P];
   const _Float16* sc = scales + static_cast<int64_t>(e) * s.H + nb * 16 + r;
 #pragma unroll
@@ -781,68 +843,78 @@ __global__ __launch_bounds__(256, 2) void moe_down_wide(const _Float16* __restri
   typename Fmt<F>::Tile tw[D][P];
   constexpr int kW = P * Fmt<F>::kTileLoads;
   auto load_w = [&](int slot_, int kt) {
+    const bool in = kt < ktiles;
+    const u32x4* pw = wp + (in ? w + kt * kstr : 0);
+    const unsigned l = in ? lane : 0;
 #pragma unroll
-    for (int p = 0; p < P; ++p) Fmt<F>::template load<true>(tw[slot_][p], w + kt * kstr + p * Fmt<F>::kTileQuads, lane);
+    for (int p = 0; p < P; ++p) Fmt<F>::template load<true>(tw[slot_][p], pw + p * Fmt<F>::kTileQuads + l, l);
   };
-  auto load_ring = [&]() {
-#pragma unroll
-    for (int d = 0; d < D; ++d) load_w(d, d < ktiles ? d : 0);
-  };
-  load_ring();
+  load_w(0, 0);
   const uint64_t mask = __ballot(ch.first >= 0);
   if (!has_work(mask, ch.first, by_pair, slot)) return;
   const int n = __popcll(mask);
   if (ch.first >= 0) col_pair[wave][__popcll(mask & ((uint64_t(1) << lane) - 1))] = static_cast<short>(ch.first);
   __builtin_amdgcn_wave_barrier();
+  half2v s2[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) s2[p] = landed(scale2_of<F>(sw[p]));
   auto pass = [&](int c0, auto C) {
     constexpr int nc = decltype(C)::value;
-    const _Float16 *srch[nc][2], *srcl[nc][2];
+    asm volatile("" : "+s"(w));
+    uint32_t at[nc][2];
+    const int64_t group = static_cast<int64_t>(t0) * s.k * s.I;
 #pragma unroll
     for (int q = 0; q < nc; ++q)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int col = 4 * wave + 2 * i + (lane >> 5), c = c0 + 16 * q + col;
-        const int64_t at = (static_cast<int64_t>(t0) * s.k + col_pair[wave][c < n ? c : c0]) * s.I + 8 * ((lane & 31) ^ (col & 7));
-        srch[q][i] = hi + at;
-        srcl[q][i] = lo + at;
+        at[q][i] = 2 * (col_pair[wave][c < n ? c : c0] * static_cast<uint32_t>(s.I) + 8 * ((lane & 31) ^ col));
       }
-    auto columns = [&](half8v* bh, half8v* bl, int kt) {
+    auto columns = [&](half8v* buf, int kt) {
+      const int64_t from = group + (kt < ktiles ? kt * 256 : 0);
 #pragma unroll
       for (int q = 0; q < nc; ++q) {
-        load_columns(bh + 512 * q, srch[q], kt, wave);
-        load_columns(bl + 512 * q, srcl[q], kt, wave);
+        load_columns(buf + 512 * q, hi + from, at[q], wave);
+        load_columns(buf + 512 * (NC + q), lo + from, at[q], wave);
       }
     };
-    columns(bufh0, bufl0, 0);
+    // In the order of the loop, which its counts rely on.
+    columns(buf0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(1, 1);
+    if constexpr (D > 2) {
+      __builtin_amdgcn_sched_barrier(0);
+      columns(buf1, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      load_w(2, 2);
+      __builtin_amdgcn_sched_barrier(0);
+      columns(buf2, 2);
+      __builtin_amdgcn_sched_barrier(0);
+      load_w(3, 3);
+    }
     __builtin_amdgcn_sched_barrier(0);
     float4v ah[nc][P], al[nc][P];
 #pragma unroll
     for (int q = 0; q < nc; ++q)
 #pragma unroll
       for (int p = 0; p < P; ++p) ah[q][p] = al[q][p] = float4v{0.f, 0.f, 0.f, 0.f};
-    auto tile = [&](int kt, auto U) {
+    auto tile = [&](int kt, auto U, auto W) {
       constexpr int u = decltype(U)::value;
-      const half8v *curh = u & 1 ? bufh1 : bufh0, *curl = u & 1 ? bufl1 : bufl0;
+      const half8v* cur = u == 0 ? buf0 : u == 1 ? buf1 : u == 2 ? buf2 : buf3;
+      half8v* next = (u + D - 1) % D == 0 ? buf0 : (u + D - 1) % D == 1 ? buf1 : (u + D - 1) % D == 2 ? buf2 : buf3;
       __builtin_amdgcn_sched_barrier(0);
-      if (kt > 0 && kt - 1 + D < ktiles) wait_vm<kW>();
-      else wait_vm<0>();
+      wait_vm<decltype(W)::value * kW + (D - 2) * 4 * nc>();
       barrier_no_fence();
-      if (kt + 1 < ktiles) {
-        if (u & 1) columns(bufh0, bufl0, kt + 1);
-        else columns(bufh1, bufl1, kt + 1);
-      }
+      columns(next, kt + D - 1);
       __builtin_amdgcn_sched_barrier(0);
-      half2v s2[P];
-#pragma unroll
-      for (int p = 0; p < P; ++p) s2[p] = scale2_of<F>(sw[p]);
       auto step = [&](auto J) {
         constexpr int j = decltype(J)::value;
-        const int at = r * 32 + ((4 * j + g) ^ (r & 7));
+        const int at = r * 32 + ((4 * j + g) ^ r);
         half8v xh[nc], xl[nc];
 #pragma unroll
         for (int q = 0; q < nc; ++q) {
-          xh[q] = curh[512 * q + at];
-          xl[q] = curl[512 * q + at];
+          xh[q] = cur[512 * q + at];
+          xl[q] = cur[512 * (NC + q) + at];
         }
 #pragma unroll
         for (int p = 0; p < P; ++p) {
@@ -859,16 +931,29 @@ __global__ __launch_bounds__(256, 2) void moe_down_wide(const _Float16* __restri
       step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
       step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
       __builtin_amdgcn_sched_barrier(0);
-      if (kt + D < ktiles) load_w(u, kt + D);
     };
-    for (int kt = 0; kt < ktiles; kt += D) {
-      tile(kt, std::integral_constant<int, 0>{});
-      if (kt + 1 < ktiles) tile(kt + 1, std::integral_constant<int, 1>{});
+    auto turn = [&](int kt, auto U) {
+      tile(kt, U, std::integral_constant<int, D - 1>{});
+      load_w(decltype(U)::value, kt + D);
+    };
+    int kt = 0;
+    for (; kt + D <= ktiles; kt += D) {
+      turn(kt, std::integral_constant<int, 0>{});
+      turn(kt + 1, std::integral_constant<int, 1>{});
       if constexpr (D > 2) {
-        if (kt + 2 < ktiles) tile(kt + 2, std::integral_constant<int, 2>{});
-        if (kt + 3 < ktiles) tile(kt + 3, std::integral_constant<int, 3>{});
+        turn(kt + 2, std::integral_constant<int, 2>{});
+        turn(kt + 3, std::integral_constant<int, 3>{});
       }
     }
+    // The rest: no weights are requested any more, or, with fewer than D k-tiles
+    // in all, not all of the ring's were.
+    constexpr std::integral_constant<int, 0> kNone{};
+    if (kt < ktiles) tile(kt, std::integral_constant<int, 0>{}, kNone);
+    if constexpr (D > 2) {
+      if (kt + 1 < ktiles) tile(kt + 1, std::integral_constant<int, 1>{}, kNone);
+      if (kt + 2 < ktiles) tile(kt + 2, std::integral_constant<int, 2>{}, kNone);
+    }
+    wait_vm<0>();  // no load into the buffers outlives its pass
 #pragma unroll
     for (int q = 0; q < nc; ++q) {
       const int c = c0 + 16 * q + r;
@@ -884,11 +969,11 @@ __global__ __launch_bounds__(256, 2) void moe_down_wide(const _Float16* __restri
     for (; n - c0 > 16; c0 += 32) {
       pass(c0, std::integral_constant<int, 2>{});
       __syncthreads();
-      if (n - c0 > 32) load_ring();
+      if (n - c0 > 32) load_w(0, 0);
     }
     if (c0 < n) pass(c0, std::integral_constant<int, 1>{});
   } else {
-    pass(0, std::integral_constant<int, 1>{});
+    pass(0, std::integral_constant<int, 1>{});  // at most 16 tokens in the group
   }
 }
 
@@ -903,14 +988,17 @@ __global__ __launch_bounds__(256) void moe_sum(const float* __restrict__ part, c
   float4v v[kMaxK];
   int id[kMaxK];
 #pragma unroll
-  for (int j = 0; j < kMaxK; ++j) id[j] = j < s.k ? ids[j] : -1;
+  for (int j = 0; j < kMaxK; ++j) {  // requested with the ids, unwritten parts too: those are not used
+    id[j] = j < s.k ? ids[j] : -1;
+    v[j] = float4v{0.f, 0.f, 0.f, 0.f};
+    if (j < s.k) v[j] = *reinterpret_cast<const float4v*>(p + static_cast<int64_t>(j) * s.H);
+  }
 #pragma unroll
   for (int j = 0; j < kMaxK; ++j) {
     bool use = id[j] >= 0 && id[j] < s.E;
 #pragma unroll
     for (int o = 0; o < j; ++o) use = use && id[o] != id[j];  // the same expert again: counted with the first
-    v[j] = float4v{0.f, 0.f, 0.f, 0.f};
-    if (use) v[j] = *reinterpret_cast<const float4v*>(p + static_cast<int64_t>(j) * s.H);
+    if (!use) v[j] = float4v{0.f, 0.f, 0.f, 0.f};
   }
   float4v sum = v[0];
 #pragma unroll
@@ -1181,14 +1269,15 @@ int launch_experts(const MoeCall& c, Route route, const _Float16* router, const 
   }
   int st = FP6_OK;
   if (wide_dn >= kWideRows * cus) {
-    // Four row blocks per wave leave no registers for two column groups.
+    // Four row blocks per wave with two column groups: no faster (75.8 us against
+    // 75.0 .. 76.5 for 64 tokens, 64 experts 2048x1024).
     const int p = wide_dn < 16 * cus ? 1 : (!two && wide_dn >= 32 * cus ? 4 : 2);
     void* args[] = {&hi, &lo, &ids, &w, &sc, &part, &s, &by_pair};
     const dim3 grid(static_cast<unsigned>(s.H / 16 / (4 * p)), grid_y, groups);
     const void* kern = p == 4   ? reinterpret_cast<const void*>(&moe_down_wide<F, 4, 2, 1>)
-                       : p == 1 ? (two ? reinterpret_cast<const void*>(&moe_down_wide<F, 1, 4, 2>)
+                       : p == 1 ? (two ? reinterpret_cast<const void*>(&moe_down_wide<F, 1, 2, 2>)
                                        : reinterpret_cast<const void*>(&moe_down_wide<F, 1, 4, 1>))
-                                : (two ? reinterpret_cast<const void*>(&moe_down_wide<F, 2, 4, 2>)
+                                : (two ? reinterpret_cast<const void*>(&moe_down_wide<F, 2, 2, 2>)
                                      : reinterpret_cast<const void*>(&moe_down_wide<F, 2, 4, 1>));
     st = moe_launch(kern, grid, dim3(256), args, c.stream);
   } else {
@@ -1314,6 +1403,16 @@ int fpx_moe_layer(int format, const void* X, const void* router, const void* gat
   const int64_t slots = T * top_k < E ? T * top_k : E;
   const bool fused = T <= kFusedT && E <= kFusedE && slots * (I / 16) < kWideRows * fpx::current_cus();
   if (fused && T * E * H <= kFusedProducts) return launch_experts_format(format, c, kFromRouter, R, nullptr, renormalize);
+  if (!fused && E <= kRouteE && E * H <= kRouteProducts && T <= 4 * fpx::current_cus()) {
+    int* oi = static_cast<int*>(ids);
+    float* ow = static_cast<float*>(weights);
+    int e = c.s.E, k = c.s.k, h = c.s.H;
+    const _Float16* x = c.X;
+    void* args[] = {&x, &R, &e, &k, &h, &renormalize, &oi, &ow};
+    st = moe_launch(reinterpret_cast<const void*>(&moe_route), dim3(static_cast<unsigned>(T)), dim3(1024), args, c.stream);
+    if (st != FP6_OK) return st;
+    return launch_experts_format(format, c, kGiven, nullptr, nullptr, 0);
+  }
   st = T <= 4 ? launch_logits<1>(c.X, R, logits, c.s, c.stream) : launch_logits<4>(c.X, R, logits, c.s, c.stream);
   if (st != FP6_OK) return st;
   if (fused) return launch_experts_format(format, c, kFromLogits, nullptr, logits, renormalize);
