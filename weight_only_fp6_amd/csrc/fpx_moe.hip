@@ -50,7 +50,8 @@ struct MoeShape {
 // Router logits in 64 bits.  A product of two fp16 numbers is exact in fp32,
 // and a sum of them in fp64 loses nothing that a choice between experts could
 // hang on: rows of equal weights tie exactly.  One workgroup per expert and TB
-// tokens, its waves and lanes split H; fixed-order sums.
+// tokens, its waves and lanes split H; fixed-order sums.  Launch and latency:
+// 64 experts x 2048, one token 2.5 us.
 // ---------------------------------------------------------------------------
 template <int TB>
 __global__ __launch_bounds__(256) void moe_logits(const _Float16* __restrict__ X, const _Float16* __restrict__ R,
@@ -149,7 +150,8 @@ __global__ __launch_bounds__(64) void moe_topk(const double* __restrict__ logits
   }
 }
 
-// Logits and choice of one token in one workgroup of 16 waves, for small routers.
+// Logits and choice of one token in one workgroup of 16 waves, for small
+// routers (16 experts x 4096, 16 tokens 6.9 us against 4.5 and 3.5).
 __global__ __launch_bounds__(1024) void moe_route(const _Float16* __restrict__ X, const _Float16* __restrict__ R, int E,
                                                   int k, int H, int renorm, int* __restrict__ ids,
                                                   float* __restrict__ weights) {
@@ -192,7 +194,10 @@ __global__ __launch_bounds__(1024) void moe_route(const _Float16* __restrict__ X
 // for all of them.  The weights run through a register ring of D k-tiles: as
 // soon as tile (row block p, k-tile t) is multiplied, tile (p, t+D) is
 // requested, so D*P tiles are in flight per wave; the token fragments of k-tile
-// t+1 are requested when k-tile t begins.
+// t+1 are requested when k-tile t begins.  Bound by latency at these sizes: one
+// token, 64 experts 2048x1024 with the choice 13.1 us (12.6 MB of weights, 1
+// TB/s); 7 tokens, 40 experts 1280x768 e2m3 10.6 us and 8.1 us for the down
+// product.
 //
 // Which expert: with fewer (token, choice) pairs than experts the grid has one
 // slot per pair, and the first pair of an expert takes it; else one slot per
@@ -977,7 +982,7 @@ __global__ __launch_bounds__(256, 2) void moe_down_wide(const _Float16* __restri
   }
 }
 
-// 4 rows of a token per thread.
+// 4 rows of a token per thread (64 tokens x 2048, 8 parts 4.5 us: launch, one load).
 __global__ __launch_bounds__(256) void moe_sum(const float* __restrict__ part, const int* __restrict__ ids,
                                                _Float16* __restrict__ Y, MoeShape s) {
   const int64_t t = blockIdx.y;
@@ -1016,7 +1021,8 @@ __global__ __launch_bounds__(256) void moe_sum(const float* __restrict__ part, c
 // a workgroup of 16 waves owns 16 rows of the output.  The columns of the MFMAs
 // are the tokens themselves, with zeros where a token did not choose the tile's
 // expert, so an output is one long product over (expert, k) and nothing but the
-// waves' sums has to be added: no parts in memory, no second kernel.  The waves
+// waves' sums has to be added: no parts in memory, no second kernel (one token,
+// 64 experts 2048x1024 9.0 us, 0.7 TB/s: a chain of ids, addresses, loads).  The waves
 // share the list of (expert, k-tile) of the experts that any token chose, in
 // the order of first choice, in equal contiguous parts, and add in wave order.
 // ---------------------------------------------------------------------------
@@ -1197,8 +1203,15 @@ int moe_launch(const void* kern, dim3 grid, dim3 block, void** args, hipStream_t
 }
 
 // Row blocks per CU, over all slots, from which on the forms with shared
-// fragments are used (4 row blocks per workgroup at least: two workgroups).
-constexpr int64_t kWideRows = 8;
+// fragments are used (4 row blocks per workgroup at least: one workgroup).  The
+// products with 4 per CU and the other forms: 64 tokens, 8 experts 4096x2048
+// 49 against 58 us; 16 tokens 43 and 42; 64 experts 2048x1024 (16 per CU) 75 and
+// 86.  With 2 per CU: 8 tokens, 4 experts 4096x2048 31 and 28, 64 tokens 60 and 62.
+constexpr int64_t kWideRows = 4;
+// Below this the choice is made in the first product, though its form with
+// shared fragments, which expects it made, would be faster by itself (2 tokens,
+// 64 experts 2048x1024, 4 per CU: 31.5 against 32.7 us).
+constexpr int64_t kFusedRows = 8;
 
 // The forms with waves that split K (fewer row blocks than the forms with
 // shared fragments want): two row blocks per wave where that still gives every
@@ -1398,10 +1411,9 @@ int fpx_moe_layer(int format, const void* X, const void* router, const void* gat
                               workspace, stream);
   double* logits = static_cast<double*>(workspace);
   const _Float16* R = static_cast<const _Float16*>(router);
-  // The choice inside the first product, where that has few row blocks (the
-  // form with shared fragments expects it made).
+  // The choice inside the first product, where that has few row blocks.
   const int64_t slots = T * top_k < E ? T * top_k : E;
-  const bool fused = T <= kFusedT && E <= kFusedE && slots * (I / 16) < kWideRows * fpx::current_cus();
+  const bool fused = T <= kFusedT && E <= kFusedE && slots * (I / 16) < kFusedRows * fpx::current_cus();
   if (fused && T * E * H <= kFusedProducts) return launch_experts_format(format, c, kFromRouter, R, nullptr, renormalize);
   if (!fused && E <= kRouteE && E * H <= kRouteProducts && T <= 4 * fpx::current_cus()) {
     int* oi = static_cast<int*>(ids);

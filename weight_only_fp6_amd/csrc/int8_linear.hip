@@ -239,6 +239,13 @@ __device__ __forceinline__ void store_tile(void* __restrict__ Y, const i32x4 (&a
 // direct loads are linear on the LDS side, so the turn is made on the global
 // side.  Kp need not be a multiple of 128: the last units of the ring are filled
 // with zeros.  Rows behind the last repeat it and are not stored.
+//
+// Few tokens are bound by the weights' bytes: 16x28672x8192 41 us, 5.7 TB/s.
+// From some hundred tokens on it is the way from the L2 to LDS that bounds, so
+// the tile is as large as registers allow (256x256 over 8 waves):
+// 4096x11008x4096 171 us, 2.16 POP/s (128x256 213 us, 128x128 222), 8192^3 421
+// us, 2.61 POP/s (556 and 588).  In between the CUs are not full and a step is
+// latency: 128x21504x7168 42 us, 168 tiles of 128x128, 3.7 TB/s (64x128 57 us).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void barrier_no_fence() { asm volatile("s_barrier" ::: "memory"); }
 
