@@ -142,6 +142,26 @@ def test_experts_uneven_routing(E, H, I):
     _run(ex, _x(T, H, 1), torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV))
 
 
+@pytest.mark.parametrize("E,T,k,H,I", [(6, 4, 2, 512, 512), (6, 16, 2, 256, 256), (40, 3, 3, 512, 256), (6, 33, 2, 512, 512),
+                                       (128, 64, 16, 512, 256)])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_experts_infinite_weights_stay_with_their_tokens(bad, E, T, k, H, I):
+    # Expert 2 is unusable; tokens that did not choose it do not notice.
+    ex = Experts(E, H, I)
+    X = _x(T, H, 8)
+    ids, w = _routing(T, E, k, 8)
+    ids[ids == 2] = 3
+    ref, bound = experts(_f64(X), ids.cpu().numpy(), _f64(w), *ex.dq)
+    args = [t.clone() for t in ex.args]
+    args[1][2] = bad
+    args[3][2] = bad
+    ids[1, k - 1] = 2
+    y = fp6.moe_experts(X, ids, w, *args)
+    others = np.arange(T) != 1
+    _check(y[torch.from_numpy(others).to(DEV)], ref[others], bound[others])
+    assert torch.isnan(y[1]).any()
+
+
 def test_experts_same_index_twice():
     ex = Experts.get(6, 512, 512)
     for T, k in ((1, 4), (5, 6), (30, 8)):

@@ -1048,18 +1048,25 @@ __global__ __launch_bounds__(1024) void moe_down_few(const _Float16* __restrict_
   struct Values {
     half8v h[8], l[8];
   };
-  auto mul = [&](const Weights& w, const Values& v) {
+  // A tile's product is added to the tokens that chose its expert only: an
+  // infinite or NaN weight times another token's zeros would be NaN.
+  auto mul = [&](const Weights& w, const Values& v, bool mine) {
     const half2v s2 = scale2_of<F>(w.scale);
+    float4v th = {0.f, 0.f, 0.f, 0.f}, tl = {0.f, 0.f, 0.f, 0.f};
     auto step = [&](auto J) {
       constexpr int j = decltype(J)::value;
       const half8v a = Fmt<F>::template step<j>(w.t, s2);
-      ah = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, v.h[j], ah, 0, 0, 0);
-      al = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, v.l[j], al, 0, 0, 0);
+      th = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, v.h[j], th, 0, 0, 0);
+      tl = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, v.l[j], tl, 0, 0, 0);
     };
     step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
     step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
     step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
     step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
+    if (mine) {
+      ah += th;
+      al += tl;
+    }
   };
   int total = s.k * ktiles;
   int f0 = wave * total / kWaves, f1 = (wave + 1) * total / kWaves;
@@ -1094,10 +1101,10 @@ __global__ __launch_bounds__(1024) void moe_down_few(const _Float16* __restrict_
       load_w(wa, f0);
       load_w(wb, f1 - 1);
       __builtin_amdgcn_sched_barrier(0);
-      mul(wa, v);
+      mul(wa, v, true);
       if (f0 + 1 < f1) {
         load_h(v, f0 + 1);
-        mul(wb, v);
+        mul(wb, v, true);
       }
     }
   } else {
@@ -1131,19 +1138,20 @@ __global__ __launch_bounds__(1024) void moe_down_few(const _Float16* __restrict_
           v.l[j] = *reinterpret_cast<const half8v*>(lo + at + 32 * j);
         }
       }
+      return mine;
     };
     // At most two tiles per wave: the second's weights are requested before the first is multiplied.
     if (f0 < f1) {
       Weights wa, wb;
       Values v;
       load_w(wa, f0);
-      load_h(v, f0);
+      bool mine = load_h(v, f0);
       load_w(wb, f1 - 1);
       __builtin_amdgcn_sched_barrier(0);
-      mul(wa, v);
+      mul(wa, v, mine);
       if (f0 + 1 < f1) {
-        load_h(v, f0 + 1);
-        mul(wb, v);
+        mine = load_h(v, f0 + 1);
+        mul(wb, v, mine);
       }
     }
   }
