@@ -196,8 +196,7 @@ __global__ __launch_bounds__(1024) void moe_route(const _Float16* __restrict__ X
 // requested, so D*P tiles are in flight per wave; the token fragments of k-tile
 // t+1 are requested when k-tile t begins.  Bound by latency at these sizes: one
 // token, 64 experts 2048x1024 with the choice 13.1 us (12.6 MB of weights, 1
-// TB/s); 7 tokens, 40 experts 1280x768 e2m3 10.6 us and 8.1 us for the down
-// product.
+// TB/s); 7 tokens, 40 experts 1280x768 e2m3, gate/up 10.6 us.
 //
 // Which expert: with fewer (token, choice) pairs than experts the grid has one
 // slot per pair, and the first pair of an expert takes it; else one slot per
@@ -482,20 +481,21 @@ __global__ __launch_bounds__(256, 2) void moe_gate_up(const _Float16* __restrict
 // add instead of a kernel of its own: 64 tokens, 64 experts 2048x1024 181 us
 // against 37.)
 // ---------------------------------------------------------------------------
-template <int F, int P, int D>
+template <int F>
 __global__ __launch_bounds__(256, 2) void moe_down(const _Float16* __restrict__ hi, const _Float16* __restrict__ lo,
                                                 const int* __restrict__ ids_g, const u32x4* __restrict__ wp,
                                                 const _Float16* __restrict__ scales, float* __restrict__ part, MoeShape s,
                                                 int ks, int by_pair) {
   __shared__ short col_pair[4][kGroup];
-  __shared__ float4v red[4][P][64];
+  constexpr int D = 2;  // k-tiles of weights in flight per wave
+  __shared__ float4v red[4][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int t0 = blockIdx.z * kGroup;
   const int tokens = s.T - t0 < kGroup ? s.T - t0 : kGroup;
   const int* ids = ids_g + static_cast<int64_t>(t0) * s.k;
   const int slot = blockIdx.y;
-  const int rows0 = blockIdx.x * (4 / ks) * P * 16;  // this workgroup's rows of the output
+  const int rows0 = blockIdx.x * (4 / ks) * 16;  // this workgroup's rows of the output
   float* parts = part + static_cast<int64_t>(t0) * s.k * s.H;
 
   int e = slot;
@@ -507,23 +507,17 @@ __global__ __launch_bounds__(256, 2) void moe_down(const _Float16* __restrict__ 
   const Choice ch = choice_of<false>(ids, nullptr, tokens, s.k, e, lane);
   const int rb = wave / ks, kslice = wave - rb * ks;
   const int ktiles = s.I >> 8;
-  const int nb = (blockIdx.x * (4 / ks) + rb) * P;
+  const int nb = blockIdx.x * (4 / ks) + rb;
   const int64_t kstr = static_cast<int64_t>(s.H >> 4) * Fmt<F>::kTileQuads;
   const u32x4* w = wp + static_cast<int64_t>(e) * ktiles * kstr + nb * static_cast<int64_t>(Fmt<F>::kTileQuads) + lane;
   const int kt0 = kslice * ktiles / ks, kt1 = (kslice + 1) * ktiles / ks;
-  typename Fmt<F>::Tile tw[D][P];
-  _Float16 sw[P];
-  const _Float16* sc = scales + static_cast<int64_t>(e) * s.H + nb * 16 + r;
+  typename Fmt<F>::Tile tw[D];
   auto load_first = [&]() {
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-        Fmt<F>::template load<true>(tw[d][p], w + (kt0 + d < kt1 ? kt0 + d : kt0) * kstr + p * Fmt<F>::kTileQuads, lane);
+    for (int d = 0; d < D; ++d) Fmt<F>::template load<true>(tw[d], w + (kt0 + d < kt1 ? kt0 + d : kt0) * kstr, lane);
   };
   load_first();
-#pragma unroll
-  for (int p = 0; p < P; ++p) sw[p] = sc[16 * p];
+  const _Float16 sw = scales[static_cast<int64_t>(e) * s.H + nb * 16 + r];
   const uint64_t mask = __ballot(ch.first >= 0);
   if (!has_work(mask, ch.first, by_pair, slot)) return;
   const int n = __popcll(mask);
@@ -544,9 +538,7 @@ __global__ __launch_bounds__(256, 2) void moe_down(const _Float16* __restrict__ 
       fh[0][j] = *reinterpret_cast<const half8v*>(hr + kt0 * 256 + 32 * j);
       fl[0][j] = *reinterpret_cast<const half8v*>(lr + kt0 * 256 + 32 * j);
     }
-    float4v ah[P], al[P];
-#pragma unroll
-    for (int p = 0; p < P; ++p) ah[p] = al[p] = float4v{0.f, 0.f, 0.f, 0.f};
+    float4v ah = {0.f, 0.f, 0.f, 0.f}, al = {0.f, 0.f, 0.f, 0.f};
     auto tile = [&](int kt, auto CUR) {
       constexpr int cur = decltype(CUR)::value;
       const int next = kt + 1 < kt1 ? kt + 1 : kt;  // behind the end: a stand-in
@@ -556,24 +548,20 @@ __global__ __launch_bounds__(256, 2) void moe_down(const _Float16* __restrict__ 
         fl[1 - cur][j] = *reinterpret_cast<const half8v*>(lr + next * 256 + 32 * j);
       }
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const half2v s2 = scale2_of<F>(sw[p]);
-        auto step = [&](auto J) {
-          constexpr int j = decltype(J)::value;
-          const half8v a = Fmt<F>::template step<j>(tw[cur % D][p], s2);
-          ah[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fh[cur][j], ah[p], 0, 0, 0);
-          al[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fl[cur][j], al[p], 0, 0, 0);
-        };
-        step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
-        step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
-        step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
-        step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
-        __builtin_amdgcn_sched_barrier(0);
-        if (kt + D < kt1)
-          Fmt<F>::template load<true>(tw[cur % D][p], w + (kt + D) * kstr + p * Fmt<F>::kTileQuads, lane);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      const half2v s2 = scale2_of<F>(sw);
+      auto step = [&](auto J) {
+        constexpr int j = decltype(J)::value;
+        const half8v a = Fmt<F>::template step<j>(tw[cur], s2);
+        ah = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fh[cur][j], ah, 0, 0, 0);
+        al = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, fl[cur][j], al, 0, 0, 0);
+      };
+      step(std::integral_constant<int, 0>{}); step(std::integral_constant<int, 1>{});
+      step(std::integral_constant<int, 2>{}); step(std::integral_constant<int, 3>{});
+      step(std::integral_constant<int, 4>{}); step(std::integral_constant<int, 5>{});
+      step(std::integral_constant<int, 6>{}); step(std::integral_constant<int, 7>{});
+      __builtin_amdgcn_sched_barrier(0);
+      if (kt + D < kt1) Fmt<F>::template load<true>(tw[cur], w + (kt + D) * kstr, lane);
+      __builtin_amdgcn_sched_barrier(0);
     };
     int kt = kt0;
     for (; kt + 2 <= kt1; kt += 2) {
@@ -581,16 +569,12 @@ __global__ __launch_bounds__(256, 2) void moe_down(const _Float16* __restrict__ 
       tile(kt + 1, std::integral_constant<int, 1>{});
     }
     if (kt < kt1) tile(kt, std::integral_constant<int, 0>{});
-#pragma unroll
-    for (int p = 0; p < P; ++p) red[wave][p][lane] = ah[p] + al[p] * (1.0f / kLoScale);
+    red[wave][lane] = ah + al * (1.0f / kLoScale);
     __syncthreads();
-    if (c0 + r < n) {
-      const int64_t dst = static_cast<int64_t>(pair) * s.H + rows0 + rb * P * 16 + 4 * g;
-      for (int p = kslice; p < P; p += ks) {
-        float4v v = red[rb * ks][p][lane];
-        for (int q = 1; q < ks; ++q) v += red[rb * ks + q][p][lane];
-        *reinterpret_cast<float4v*>(parts + dst + 16 * p) = v;
-      }
+    if (kslice == 0 && c0 + r < n) {
+      float4v v = red[rb * ks][lane];
+      for (int q = 1; q < ks; ++q) v += red[rb * ks + q][lane];
+      *reinterpret_cast<float4v*>(parts + static_cast<int64_t>(pair) * s.H + rows0 + rb * 16 + 4 * g) = v;
     }
   }
 }
@@ -1221,17 +1205,8 @@ constexpr int64_t kWideRows = 4;
 // 64 experts 2048x1024, 4 per CU: 31.5 against 32.7 us).
 constexpr int64_t kFusedRows = 8;
 
-// The forms with waves that split K (fewer row blocks than the forms with
-// shared fragments want): two row blocks per wave where that still gives every
-// CU two workgroups, counting every slot as used.
-struct Split {
-  int ks, p;
-};
-Split choose_split(int64_t row_blocks, int64_t ktiles, int64_t slots, int cus) {
-  Split s{4, slots * (row_blocks / 2) >= 2 * cus ? 2 : 1};
-  while (s.ks > ktiles) s.ks >>= 1;
-  return s;
-}
+// Waves that split K in the forms with fewer row blocks.
+int k_slices(int64_t ktiles) { return ktiles >= 4 ? 4 : ktiles >= 2 ? 2 : 1; }
 
 // route: where the choice comes from; all but kGiven make it in the first product.
 template <int F>
@@ -1263,19 +1238,21 @@ int launch_experts(const MoeCall& c, Route route, const _Float16* router, const 
     const int st = moe_launch(kern, grid, dim3(256), args, c.stream);
     if (st != FP6_OK) return st;
   } else {
-    Split sp = choose_split(s.I / 16, s.H / 256, slots, cus);
-    void* args[] = {&X, &router, &logits, &ids, &weights, &w, &sc, &hi, &lo, &s, &sp.ks, &by_pair, &renorm};
-    const dim3 grid(static_cast<unsigned>(s.I / 16 / (4 / sp.ks * sp.p)), grid_y, groups);
+    // Two row blocks per wave where that still gives every CU two workgroups,
+    // counting every slot as used.
+    int ks = k_slices(s.H / 256);
+    const int p = route != kGiven && wide_gu >= 4 * cus ? 2 : 1;
+    void* args[] = {&X, &router, &logits, &ids, &weights, &w, &sc, &hi, &lo, &s, &ks, &by_pair, &renorm};
+    const dim3 grid(static_cast<unsigned>(s.I / 16 / (4 / ks * p)), grid_y, groups);
     const void* kern = nullptr;
     if (route == kFromRouter)
-      kern = sp.p == 2 ? reinterpret_cast<const void*>(&moe_gate_up<F, 2, 1, kFromRouter>)
-                       : reinterpret_cast<const void*>(&moe_gate_up<F, 1, 2, kFromRouter>);
+      kern = p == 2 ? reinterpret_cast<const void*>(&moe_gate_up<F, 2, 1, kFromRouter>)
+                    : reinterpret_cast<const void*>(&moe_gate_up<F, 1, 2, kFromRouter>);
     else if (route == kFromLogits)
-      kern = sp.p == 2 ? reinterpret_cast<const void*>(&moe_gate_up<F, 2, 1, kFromLogits>)
-                       : reinterpret_cast<const void*>(&moe_gate_up<F, 1, 2, kFromLogits>);
+      kern = p == 2 ? reinterpret_cast<const void*>(&moe_gate_up<F, 2, 1, kFromLogits>)
+                    : reinterpret_cast<const void*>(&moe_gate_up<F, 1, 2, kFromLogits>);
     else
-      kern = sp.p == 2 ? reinterpret_cast<const void*>(&moe_gate_up<F, 2, 1, kGiven>)
-                       : reinterpret_cast<const void*>(&moe_gate_up<F, 1, 2, kGiven>);
+      kern = reinterpret_cast<const void*>(&moe_gate_up<F, 1, 2, kGiven>);
     const int st = moe_launch(kern, grid, dim3(256), args, c.stream);
     if (st != FP6_OK) return st;
   }
@@ -1302,12 +1279,10 @@ int launch_experts(const MoeCall& c, Route route, const _Float16* router, const 
                                      : reinterpret_cast<const void*>(&moe_down_wide<F, 2, 4, 1>));
     st = moe_launch(kern, grid, dim3(256), args, c.stream);
   } else {
-    Split sp = choose_split(s.H / 16, s.I / 256, slots, cus);
-    void* args[] = {&hi, &lo, &ids, &w, &sc, &part, &s, &sp.ks, &by_pair};
-    const dim3 grid(static_cast<unsigned>(s.H / 16 / (4 / sp.ks * sp.p)), grid_y, groups);
-    const void* kern = sp.p == 2 ? reinterpret_cast<const void*>(&moe_down<F, 2, 1>)
-                                 : reinterpret_cast<const void*>(&moe_down<F, 1, 2>);
-    st = moe_launch(kern, grid, dim3(256), args, c.stream);
+    int ks = k_slices(s.I / 256);
+    void* args[] = {&hi, &lo, &ids, &w, &sc, &part, &s, &ks, &by_pair};
+    const dim3 grid(static_cast<unsigned>(s.H / 16 / (4 / ks)), grid_y, groups);
+    st = moe_launch(reinterpret_cast<const void*>(&moe_down<F>), grid, dim3(256), args, c.stream);
   }
   if (st != FP6_OK) return st;
   void* sum_args[] = {&part, &ids, &Y, &s};
